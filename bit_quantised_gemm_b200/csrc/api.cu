@@ -431,6 +431,221 @@ int kv_attention_3bit(const uint16_t* q, int64_t B, int64_t H, int64_t D, int64_
   return e == cudaSuccess ? ok() : cuda_fail(e, "kv_attention_3bit", why);
 }
 
+// ------------------------------------------------------- paged 3-bit cache
+int64_t kv_page_block_bytes(int64_t D) {
+  return D == 64 || D == 128 || D == 256 ? BITLINEAR_PAGE_TOKENS * (3 * D / 4 + 8) : 0;
+}
+
+// One layer's pool as the append and the attention take it.
+static int check_pool(const char* fn, const uint8_t* pages, int64_t n_pages, int64_t H, int64_t D,
+                      const uint8_t* codes4, int64_t C4) {
+  if (D != 64 && D != 128 && D != 256) return fail(BITLINEAR_ERR_UNSUPPORTED, "%s: D must be 64, 128 or 256", fn);
+  if (H <= 0 || H > 65535) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: H must lie in 1..65535", fn);
+  if (n_pages < 0 || n_pages >= (1LL << 31) / BITLINEAR_PAGE_TOKENS)
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: n_pages must lie in 0..2^25 - 1", fn);
+  if (C4 < 0 || C4 > BITLINEAR_PAGE_TOKENS) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: C4 must lie in 0..64", fn);
+  if (n_pages > 0 && (!pages || (C4 > 0 && !codes4))) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: null pool pointer", fn);
+  if (!aligned16(pages) || (C4 > 0 && !aligned16(codes4)))
+    return fail(BITLINEAR_ERR_ALIGNMENT, "%s: the pool must be 16-byte aligned", fn);
+  return BITLINEAR_OK;
+}
+
+int kv_append_3bit(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, int64_t n, int64_t H,
+                   int64_t D, const int32_t* slots, const int32_t* row4, uint8_t* pages, int64_t n_pages,
+                   uint8_t* codes4, int64_t C4, int* dev_status, bitlinear_stream_t stream) {
+  const char* fn = "kv_append_3bit";
+  const int rc = check_pool(fn, pages, n_pages, H, D, codes4, C4);
+  if (rc != BITLINEAR_OK) return rc;
+  if (n < 0) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: bad number of tokens", fn);
+  if (ldk < H * D || ldv < H * D || ldk % 8 != 0 || ldv % 8 != 0)
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: ldk and ldv must be >= H D and multiples of 8", fn);
+  if (n > 0x7FFFFFFF || n * H * D >= (1LL << 40)) return fail(BITLINEAR_ERR_UNSUPPORTED, "%s: too many tokens", fn);
+  if (n == 0) return ok();
+  if (!k || !v || !slots) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned16(k) || !aligned16(v)) return fail(BITLINEAR_ERR_ALIGNMENT, "%s: k and v must be 16-byte aligned", fn);
+  blt::paged::AppendArgs a{k, v, ldk, ldv, n, H, slots, row4, pages, n_pages, codes4, C4, dev_status};
+  cudaError_t e = blt::launch_paged_append(a, D, stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_append_3bit launch");
+}
+
+// A pool of L layers as the page calls take it.
+static int check_pages(const char* fn, const uint8_t* pages, int64_t page_bytes, const uint8_t* codes4,
+                       int64_t page_bytes4, int64_t L, int64_t n_pages) {
+  if (L < 0 || n_pages < 0 || n_pages >= (1LL << 31) / BITLINEAR_PAGE_TOKENS)
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: L must be >= 0 and n_pages lie in 0..2^25 - 1", fn);
+  if (page_bytes <= 0 || page_bytes4 < 0 || page_bytes % 16 != 0 || page_bytes4 % 16 != 0)
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: page_bytes and page_bytes4 must be multiples of 16", fn);
+  if (page_bytes >= (1LL << 31) || page_bytes4 >= (1LL << 31) || L > 65535)
+    return fail(BITLINEAR_ERR_UNSUPPORTED, "%s: sizes beyond the supported range", fn);
+  if (L > 0 && n_pages > 0 && (!pages || (page_bytes4 > 0 && !codes4)))
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: null pool pointer", fn);
+  if (!aligned16(pages) || (page_bytes4 > 0 && !aligned16(codes4)))
+    return fail(BITLINEAR_ERR_ALIGNMENT, "%s: the pool must be 16-byte aligned", fn);
+  return BITLINEAR_OK;
+}
+
+static int check_tables(const char* fn, const int32_t* tables, int64_t R, int64_t W, int64_t ldt,
+                        const int32_t* lens, const int32_t* refs, int64_t n_pages, int* dev_status,
+                        blt::paged::TableArgs* t) {
+  if (R < 0 || W < 0 || R > 0x7FFFFFFF || W >= (1LL << 31) / BITLINEAR_PAGE_TOKENS || ldt < W)
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: bad table sizes (R, W >= 0, W < 2^25, ldt >= W)", fn);
+  if (n_pages < 0 || n_pages >= (1LL << 31) / BITLINEAR_PAGE_TOKENS)
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: n_pages must lie in 0..2^25 - 1", fn);
+  if ((R > 0 && (!lens || (W > 0 && !tables))) || (n_pages > 0 && !refs))
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: null table pointer", fn);
+  *t = blt::paged::TableArgs{const_cast<int32_t*>(tables), ldt, static_cast<int>(R), static_cast<int>(W),
+                             const_cast<int32_t*>(lens), const_cast<int32_t*>(refs), static_cast<int>(n_pages),
+                             dev_status};
+  return BITLINEAR_OK;
+}
+
+int kv_pages_copy(uint8_t* pages, int64_t page_bytes, uint8_t* codes4, int64_t page_bytes4, int64_t L,
+                  int64_t n_pages, const int32_t* src, const int32_t* dst, int64_t n, int* dev_status,
+                  bitlinear_stream_t stream) {
+  const char* fn = "kv_pages_copy";
+  const int rc = check_pages(fn, pages, page_bytes, codes4, page_bytes4, L, n_pages);
+  if (rc != BITLINEAR_OK) return rc;
+  if (n < 0 || n > 0x7FFFFFFF) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: bad number of pairs", fn);
+  if (n == 0 || L == 0) return ok();
+  if (!src || !dst) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: null pointer", fn);
+  blt::paged::CopyArgs a{pages, codes4, L, n_pages, page_bytes, page_bytes4, src, dst, n, nullptr, dev_status};
+  cudaError_t e = blt::launch_pages_copy(a, stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_copy launch");
+}
+
+int kv_pages_fork(int32_t* tables, int64_t R, int64_t W, int64_t ldt, int32_t* lens, int32_t* refs,
+                  int64_t n_pages, const int32_t* parents, const int32_t* children, int64_t n, int* dev_status,
+                  bitlinear_stream_t stream) {
+  const char* fn = "kv_pages_fork";
+  blt::paged::TableArgs t{};
+  const int rc = check_tables(fn, tables, R, W, ldt, lens, refs, n_pages, dev_status, &t);
+  if (rc != BITLINEAR_OK) return rc;
+  if (n < 0) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: bad number of entries", fn);
+  if (n > 65535) return fail(BITLINEAR_ERR_UNSUPPORTED, "%s: at most 65535 entries", fn);
+  if (n == 0) return ok();
+  if (!parents || !children) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: null pointer", fn);
+  cudaError_t e = blt::launch_pages_fork(t, parents, children, n, stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_fork launch");
+}
+
+int kv_pages_grow(uint8_t* pages, int64_t page_bytes, uint8_t* codes4, int64_t page_bytes4, int64_t L,
+                  int64_t n_pages, int32_t* tables, int64_t R, int64_t W, int64_t ldt, int32_t* lens,
+                  int32_t* refs, const int32_t* rows, const int32_t* n_new, int64_t n, int64_t max_new,
+                  int32_t* slots, int32_t* work, int* dev_status, bitlinear_stream_t stream) {
+  const char* fn = "kv_pages_grow";
+  int rc = check_pages(fn, pages, page_bytes, codes4, page_bytes4, L, n_pages);
+  if (rc != BITLINEAR_OK) return rc;
+  blt::paged::TableArgs t{};
+  rc = check_tables(fn, tables, R, W, ldt, lens, refs, n_pages, dev_status, &t);
+  if (rc != BITLINEAR_OK) return rc;
+  if (n < 0 || max_new < 0) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: bad number of entries or tokens", fn);
+  if (n > 1024) return fail(BITLINEAR_ERR_UNSUPPORTED, "%s: at most 1024 entries", fn);
+  if (n * max_new > 0x7FFFFFFF) return fail(BITLINEAR_ERR_UNSUPPORTED, "%s: too many slots", fn);
+  if (n == 0) return ok();
+  if (!rows || !n_new || !work || (max_new > 0 && !slots)) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: null pointer", fn);
+  blt::paged::CopyArgs c{pages, codes4, L, n_pages, page_bytes, page_bytes4, nullptr, nullptr, 0, nullptr, dev_status};
+  cudaError_t e = blt::launch_pages_grow(t, rows, n_new, n, max_new, slots, work, c, stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_grow launch");
+}
+
+int kv_pages_free(int32_t* tables, int64_t R, int64_t W, int64_t ldt, int32_t* lens, int32_t* refs,
+                  int64_t n_pages, const int32_t* rows, const int32_t* keep, int64_t n, int* dev_status,
+                  bitlinear_stream_t stream) {
+  const char* fn = "kv_pages_free";
+  blt::paged::TableArgs t{};
+  const int rc = check_tables(fn, tables, R, W, ldt, lens, refs, n_pages, dev_status, &t);
+  if (rc != BITLINEAR_OK) return rc;
+  if (n < 0) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: bad number of entries", fn);
+  if (n > 65535) return fail(BITLINEAR_ERR_UNSUPPORTED, "%s: at most 65535 entries", fn);
+  if (n == 0) return ok();
+  if (!rows) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: null pointer", fn);
+  cudaError_t e = blt::launch_pages_free(t, rows, keep, n, stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_free launch");
+}
+
+int kv_pages_compact(uint8_t* pages, int64_t page_bytes, uint8_t* codes4, int64_t page_bytes4, int64_t L,
+                     int64_t n_pages, int32_t* tables, int64_t R, int64_t W, int64_t ldt, int32_t* lens,
+                     int32_t* refs, int32_t* n_live, int32_t* work, int* dev_status, bitlinear_stream_t stream) {
+  const char* fn = "kv_pages_compact";
+  int rc = check_pages(fn, pages, page_bytes, codes4, page_bytes4, L, n_pages);
+  if (rc != BITLINEAR_OK) return rc;
+  blt::paged::TableArgs t{};
+  rc = check_tables(fn, tables, R, W, ldt, lens, refs, n_pages, dev_status, &t);
+  if (rc != BITLINEAR_OK) return rc;
+  if (!n_live || !work) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: null pointer", fn);
+  blt::paged::CopyArgs c{pages, codes4, L, n_pages, page_bytes, page_bytes4, nullptr, nullptr, 0, nullptr, dev_status};
+  cudaError_t e = blt::launch_pages_compact(t, c, work, n_live, stream);
+  return e == cudaSuccess ? ok() : cuda_fail(e, "kv_pages_compact launch");
+}
+
+static int check_paged_attention(const char* fn, int64_t B, int64_t Sq, int64_t Hq, int64_t H, int64_t D,
+                                 int64_t n_shared, int64_t W) {
+  if (B < 0 || Sq <= 0 || H <= 0 || Hq <= 0 || n_shared < 0 || W < 0)
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: bad sizes", fn);
+  if (Hq % H != 0) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: Hq must be a multiple of H", fn);
+  if (D != 64 && D != 128 && D != 256) return fail(BITLINEAR_ERR_UNSUPPORTED, "%s: D must be 64, 128 or 256", fn);
+  if (B > 65535 || Sq > 128 || Hq > 65535 || B * Sq * Hq >= (1LL << 31) / 256 ||
+      n_shared + W >= (1LL << 31) / BITLINEAR_PAGE_TOKENS)
+    return fail(BITLINEAR_ERR_UNSUPPORTED, "%s: sizes beyond the supported range", fn);
+  return BITLINEAR_OK;
+}
+
+int64_t kv_attention_3bit_paged_workspace(int64_t B, int64_t Sq, int64_t Hq, int64_t H, int64_t D,
+                                          int64_t n_shared, int64_t W) {
+  const int rc = check_paged_attention("kv_attention_3bit_paged_workspace", B, Sq, Hq, H, D, n_shared, W);
+  if (rc != BITLINEAR_OK) return rc;
+  ok();
+  return B == 0 ? 0 : blt::paged_attention_workspace(B, Sq, Hq, H, D, n_shared, W);
+}
+
+int kv_attention_3bit_paged(const uint16_t* q, int64_t ldq, int64_t B, int64_t Sq, int64_t Hq, int64_t H,
+                            int64_t D, const uint8_t* pages, int64_t n_pages, const uint8_t* codes4, int64_t C4,
+                            const int32_t* shared, int64_t n_shared, const int32_t* tables, int64_t W,
+                            int64_t ldt, const int32_t* lens, uint16_t* out, void* work, int64_t work_bytes,
+                            int* dev_status, bitlinear_stream_t stream) {
+  const char* fn = "kv_attention_3bit_paged";
+  int rc = check_paged_attention(fn, B, Sq, Hq, H, D, n_shared, W);
+  if (rc != BITLINEAR_OK) return rc;
+  rc = check_pool(fn, pages, n_pages, H, D, codes4, C4);
+  if (rc != BITLINEAR_OK) return rc;
+  if (ldq < Hq * D || ldq % 8 != 0) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: ldq must be >= Hq D and a multiple of 8", fn);
+  if (ldt < W) return fail(BITLINEAR_ERR_INVALID_ARG, "%s: ldt must be >= W", fn);
+  if (B == 0) return ok();
+  if (!q || !lens || !out || (n_shared > 0 && !shared) || (W > 0 && !tables))
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned16(q) || !aligned16(out) || !aligned16(work))
+    return fail(BITLINEAR_ERR_ALIGNMENT, "%s: q, out and work must be 16-byte aligned", fn);
+  const int64_t need = blt::paged_attention_workspace(B, Sq, Hq, H, D, n_shared, W);
+  if (work_bytes < need || (need > 0 && !work))
+    return fail(BITLINEAR_ERR_INVALID_ARG, "%s: a workspace of %lld bytes, %lld needed", fn, (long long)work_bytes, (long long)need);
+  blt::paged::AttnArgs a{};
+  a.q = q;
+  a.ldq = ldq;
+  a.B = static_cast<int>(B);
+  a.Sq = static_cast<int>(Sq);
+  a.Hq = static_cast<int>(Hq);
+  a.H = static_cast<int>(H);
+  a.D = static_cast<int>(D);
+  a.pages = pages;
+  a.n_pages = static_cast<int>(n_pages);
+  a.codes4 = codes4;
+  a.C4 = static_cast<int>(C4);
+  a.shared = shared;
+  a.n_shared = static_cast<int>(n_shared);
+  a.tables = tables;
+  a.ldt = ldt;
+  a.W = static_cast<int>(W);
+  a.lens = lens;
+  a.qk_scale = static_cast<float>(1.0 / std::sqrt(static_cast<double>(D)));
+  a.out = out;
+  a.work = static_cast<uint8_t*>(work);
+  a.status = dev_status;
+  a.timeout_ns = static_cast<uint64_t>(g_timeout_ns.load(std::memory_order_relaxed));
+  const char* why = nullptr;
+  cudaError_t e = blt::launch_paged_attention(a, stream, &why);
+  return e == cudaSuccess ? ok() : cuda_fail(e, fn, why);
+}
+
 int bitlinear_tensor_peak(int kind, int iters, uint64_t* ns_out, int* units_out, int* dev_status,
                           bitlinear_stream_t stream) {
   if (kind < 0 || kind > 2) return fail(BITLINEAR_ERR_INVALID_ARG, "tensor_peak: kind must be 0, 1 or 2");
@@ -453,6 +668,9 @@ int bitlinear_check_status(const int* dev_status, bitlinear_stream_t stream) {
   e = cudaMemcpy(&h, dev_status, sizeof(int), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return cuda_fail(e, "check_status read");
   if (h & BITLINEAR_STATUS_TIMEOUT) return fail(BITLINEAR_ERR_TIMEOUT, "a kernel gave up a bounded wait");
+  if (h & BITLINEAR_STATUS_BAD_INDEX)
+    return fail(BITLINEAR_ERR_INDEX, "a kernel met an index (page, slot, row or length) outside its tensors");
+  if (h & BITLINEAR_STATUS_NO_PAGES) return fail(BITLINEAR_ERR_NO_PAGES, "fewer free pages than wanted");
   return ok();
 }
 

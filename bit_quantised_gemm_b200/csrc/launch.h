@@ -26,6 +26,78 @@ cudaError_t launch_kv_quant_pair(const uint16_t* k, const uint16_t* v, int64_t T
                                  const int32_t* keep4, int64_t n4, uint8_t* k3, uint8_t* k4, float* ks,
                                  uint8_t* v3, uint8_t* v4, float* vs, cudaStream_t s);
 
+// The paged 3-bit cache (paged.cu, paged_attn.cu).
+namespace paged {
+struct AppendArgs {
+  const uint16_t* k;     // bf16 [n][H][D], tokens ldk apart
+  const uint16_t* v;
+  int64_t ldk, ldv;
+  int64_t n, H;
+  const int32_t* slots;  // [n]
+  const int32_t* row4;   // [n] or null
+  uint8_t* pages;
+  int64_t n_pages;
+  uint8_t* codes4;
+  int64_t C4;
+  int* status;
+};
+struct CopyArgs {
+  uint8_t* pages;        // [L][n_pages][page_bytes]
+  uint8_t* codes4;       // [L][n_pages][page_bytes4]
+  int64_t L, n_pages, page_bytes, page_bytes4;
+  const int32_t* src;    // [n]
+  const int32_t* dst;
+  int64_t n;
+  const int32_t* count;  // device, or null: only the first *count pairs
+  int* status;
+};
+struct TableArgs {
+  int32_t* tables;       // [R][W], rows ldt apart
+  int64_t ldt;
+  int R, W;
+  int32_t* lens;         // [R]
+  int32_t* refs;         // [n_pages]
+  int n_pages;
+  int* status;
+};
+struct AttnArgs {
+  const uint16_t* q;     // bf16 [B][Sq][Hq][D], tokens (b, i) ldq apart
+  int64_t ldq;
+  int B, Sq, Hq, H, D;
+  const uint8_t* pages;
+  int n_pages;
+  const uint8_t* codes4;
+  int C4;
+  const int32_t* shared; // [n_shared]
+  int n_shared;
+  const int32_t* tables; // [B][W], rows ldt apart
+  int64_t ldt;
+  int W;
+  const int32_t* lens;   // [B]
+  float qk_scale;        // 1 / sqrt(D)
+  uint16_t* out;         // bf16 [B][Sq][Hq][D]
+  uint8_t* work;
+  int* status;
+  uint64_t timeout_ns;
+};
+}  // namespace paged
+cudaError_t launch_paged_append(const paged::AppendArgs& a, int64_t D, cudaStream_t s);
+cudaError_t launch_pages_copy(const paged::CopyArgs& a, cudaStream_t s);
+cudaError_t launch_pages_fork(const paged::TableArgs& t, const int32_t* parents, const int32_t* children, int64_t n,
+                              cudaStream_t s);
+cudaError_t launch_pages_free(const paged::TableArgs& t, const int32_t* rows, const int32_t* keep, int64_t n,
+                              cudaStream_t s);
+// cow: device int32 [2 n], the pages copied on write (source, destination; -1: none)
+cudaError_t launch_pages_grow(const paged::TableArgs& t, const int32_t* rows, const int32_t* n_new, int64_t n,
+                              int64_t max_new, int32_t* slots, int32_t* cow, const paged::CopyArgs& c,
+                              cudaStream_t s);
+// work: device int32 [2 n_pages + 3]
+cudaError_t launch_pages_compact(const paged::TableArgs& t, const paged::CopyArgs& c, int32_t* work,
+                                 int32_t* n_live, cudaStream_t s);
+int64_t paged_attention_workspace(int64_t B, int64_t Sq, int64_t Hq, int64_t H, int64_t D, int64_t n_shared,
+                                  int64_t W);
+cudaError_t launch_paged_attention(const paged::AttnArgs& a, cudaStream_t s, const char** why);
+
 // Epilogue of the GEMM kernels.
 enum OutMode : int { kOutBf16 = 0, kOutRaw = 1 };
 

@@ -26,8 +26,10 @@
  *     process may drive several GPUs.
  *   - dev_status (nullable, device int): a kernel that gives up a bounded
  *     wait ORs BITLINEAR_STATUS_TIMEOUT into it and returns early; the
- *     output is then undefined. The caller zeroes it; read it with
- *     bitlinear_check_status().
+ *     output is then undefined. The paged-cache calls also report indexes
+ *     that lie outside their tensors (BITLINEAR_STATUS_BAD_INDEX) and a pool
+ *     without enough free pages (BITLINEAR_STATUS_NO_PAGES). The caller
+ *     zeroes it; read it with bitlinear_check_status().
  */
 #ifndef BITLINEAR_H
 #define BITLINEAR_H
@@ -46,12 +48,14 @@ enum {
   BITLINEAR_ERR_ALIGNMENT = -2,
   BITLINEAR_ERR_UNSUPPORTED = -3,
   BITLINEAR_ERR_CUDA = -4,
-  BITLINEAR_ERR_TIMEOUT = -5
+  BITLINEAR_ERR_TIMEOUT = -5,
+  BITLINEAR_ERR_INDEX = -6,   /* a kernel met an index outside its tensors */
+  BITLINEAR_ERR_NO_PAGES = -7 /* fewer free pages than wanted */
 };
 
 enum { BITLINEAR_MODE_INT8 = 0, BITLINEAR_MODE_INT4 = 1, BITLINEAR_MODE_FP4 = 2 };
 
-enum { BITLINEAR_STATUS_TIMEOUT = 1 };
+enum { BITLINEAR_STATUS_TIMEOUT = 1, BITLINEAR_STATUS_BAD_INDEX = 2, BITLINEAR_STATUS_NO_PAGES = 4 };
 
 /* Message for the last error returned on this thread ("" if none). */
 const char* bitlinear_last_error(void);
@@ -258,6 +262,172 @@ int kv_attention_3bit(const uint16_t* q, int64_t B, int64_t H, int64_t D, int64_
                       bitlinear_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The paged 3-bit KV cache: the kv_quant_3bit storage ([R] "Эксперименты":
+ * 3-bit KV cache, <bos> and <eos> kept at 4 bits) in pages of
+ * BITLINEAR_PAGE_TOKENS tokens, for batches of sequences that grow, fork and
+ * end, and that may share the pages of a common prefix.
+ *
+ * Pool of one layer: `pages`, device uint8 [n_pages x H x block] with
+ * block = kv_page_block_bytes(D); the block of a (page, head) holds, with
+ * RB = 3D/8,
+ *   bytes [0, 64 RB)        K codes: row o (the page's token o) at o RB, the
+ *                           little-endian 3-bit stream of kv_quant_3bit
+ *   bytes [64 RB, 128 RB)   V codes: byte i of token o's row at
+ *                           64 RB + (o / 4) 4 RB + 4 i + o % 4
+ *   fp32 [64], fp32 [64]    K scales, V scales
+ * A token kept at 4 bits has its K scale stored negated, zero bytes for its
+ * 3-bit rows but for byte 0 of the K row, which is j, and its 4-bit rows in
+ * row j of `codes4`, device uint8 [n_pages x H x C4 x D]: K's D/2 bytes, then
+ * V's (code + 8, low nibble first). C4 (0..64, 0: no codes4) is the pool's
+ * number of 4-bit rows a page.
+ * A pool of L layers holds the layers' pools one behind the other:
+ * [L x n_pages x H x block]; page p means page p of every layer.
+ *
+ * Sequences: row r of `tables`, device int32 [R x W] with rows ldt apart,
+ * lists the pages of sequence r: its token t lies in page tables[r][t / 64].
+ * lens[r] is its number of tokens (0: none); the entries behind its last page
+ * say nothing. refs[p] is how many table entries name page p; a page is free
+ * exactly when refs[p] == 0.
+ *
+ * Indexes in device memory cannot be checked on the host: an entry that lies
+ * outside its tensor is left out (never accessed) and reported in dev_status.
+ * Calls that share a pool or its tables are ordered by their stream, or by
+ * the caller.
+ * ---------------------------------------------------------------------------
+ */
+#define BITLINEAR_PAGE_TOKENS 64
+
+/* Bytes of the block of a (page, head): 64 (3D/4 + 8); 0 if D is none of
+ * 64, 128, 256. */
+int64_t kv_page_block_bytes(int64_t D);
+
+/*
+ * Quantise new tokens into a pool: token i of k and v is written to slot
+ * slots[i] = page * 64 + place in the page, exactly as kv_quant_3bit
+ * quantises it (4 bits where row4[i] >= 0).
+ *   k, v     device bf16 [n x H x D], tokens ldk / ldv elements apart (slices
+ *            of a fused projection's output will do)
+ *   slots    device int32 [n]; negative: the token is left out. Slots that
+ *            are not negative are distinct
+ *   row4     device int32 [n], nullable: the 4-bit row of the token's page
+ *            that takes token i, 0 .. C4 - 1, or negative: 3 bits. Tokens of
+ *            one page have distinct rows
+ *   pages, codes4   one layer's pool, written; codes4 nullable iff C4 == 0
+ * Requires D in {64, 128, 256}, ldk, ldv >= H D and multiples of 8, k, v,
+ * pages, codes4 16-byte aligned, finite values (a row with others is stored
+ * as some row).
+ */
+int kv_append_3bit(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, int64_t n,
+                   int64_t H, int64_t D, const int32_t* slots, const int32_t* row4, uint8_t* pages,
+                   int64_t n_pages, uint8_t* codes4, int64_t C4, int* dev_status,
+                   bitlinear_stream_t stream);
+
+/*
+ * Copy page src[i] onto page dst[i], in all L layers.
+ *   pages    device uint8 [L x n_pages x page_bytes], page_bytes = H * block
+ *   codes4   device uint8 [L x n_pages x page_bytes4], page_bytes4 = H C4 D;
+ *            nullable iff page_bytes4 == 0
+ *   src, dst device int32 [n]; a pair of two negative pages is left out. No
+ *            page is the destination of two pairs, or source and destination
+ * Requires page_bytes, page_bytes4 multiples of 16 and 16-byte aligned pools.
+ */
+int kv_pages_copy(uint8_t* pages, int64_t page_bytes, uint8_t* codes4, int64_t page_bytes4,
+                  int64_t L, int64_t n_pages, const int32_t* src, const int32_t* dst, int64_t n,
+                  int* dev_status, bitlinear_stream_t stream);
+
+/*
+ * Fork sequences: row children[i] becomes the sequence of row parents[i],
+ * on the same pages (their reference counts rise by one).
+ *   parents, children  device int32 [n], n <= 65535
+ * A child holds no tokens before, and no entry's parent is among the
+ * children: entries that break this are left out and reported. Of the entries
+ * that name one child the first counts, the others are left out and reported.
+ */
+int kv_pages_fork(int32_t* tables, int64_t R, int64_t W, int64_t ldt, int32_t* lens, int32_t* refs,
+                  int64_t n_pages, const int32_t* parents, const int32_t* children, int64_t n,
+                  int* dev_status, bitlinear_stream_t stream);
+
+/*
+ * Make room for n_new[i] more tokens of row rows[i], and list their slots.
+ * The entries are served as if one after the other: a partly filled last
+ * page with another reference is left to the others and copied to a new page
+ * (in all L layers); further pages follow as the tokens need them. New pages
+ * are the lowest free ones. If the pool has fewer free pages than all entries
+ * need, none is served (BITLINEAR_STATUS_NO_PAGES): lengths, references and
+ * the tables' entries of the sequences stay, and all slots are negative.
+ *   pages, codes4, L, page_bytes, page_bytes4   as for kv_pages_copy
+ *   rows     device int32 [n], n <= 1024, distinct: a row named again is left
+ *            out and reported
+ *   n_new    device int32 [n], each 0 .. max_new
+ *   slots    device int32 [n x max_new], written: the slots of row rows[i]'s
+ *            new tokens, then -1: what kv_append_3bit takes
+ *   work     device int32 [2 n], written
+ * Rows whose tokens would not fit into W pages are left out and reported.
+ */
+int kv_pages_grow(uint8_t* pages, int64_t page_bytes, uint8_t* codes4, int64_t page_bytes4,
+                  int64_t L, int64_t n_pages, int32_t* tables, int64_t R, int64_t W, int64_t ldt,
+                  int32_t* lens, int32_t* refs, const int32_t* rows, const int32_t* n_new,
+                  int64_t n, int64_t max_new, int32_t* slots, int32_t* work, int* dev_status,
+                  bitlinear_stream_t stream);
+
+/*
+ * End sequences, or take back their last tokens: row rows[i] keeps its first
+ * keep[i] tokens (0 where keep is NULL; all where it has no more), and the
+ * pages behind them lose its reference. A row named again counts once.
+ *   rows, keep  device int32 [n], n <= 65535; keep nullable, not negative
+ */
+int kv_pages_free(int32_t* tables, int64_t R, int64_t W, int64_t ldt, int32_t* lens, int32_t* refs,
+                  int64_t n_pages, const int32_t* rows, const int32_t* keep, int64_t n,
+                  int* dev_status, bitlinear_stream_t stream);
+
+/*
+ * Move the n_live pages in use to the front of the pool: the k-th free page
+ * below n_live takes the k-th page in use at or above it (in all L layers),
+ * and the tables of all R rows follow.
+ *   n_live   device int32 [1], written: the pages from n_live on are free
+ *   work     device int32 [2 n_pages + 3], written
+ */
+int kv_pages_compact(uint8_t* pages, int64_t page_bytes, uint8_t* codes4, int64_t page_bytes4,
+                     int64_t L, int64_t n_pages, int32_t* tables, int64_t R, int64_t W, int64_t ldt,
+                     int32_t* lens, int32_t* refs, int32_t* n_live, int32_t* work, int* dev_status,
+                     bitlinear_stream_t stream);
+
+/*
+ * Decode attention over a paged cache, the pages of a shared prefix read once
+ * for the whole batch. Sequence b has lens[b] tokens, of which the last Sq are
+ * its queries' own (already appended): token t lies in page shared[t / 64]
+ * while t < 64 n_shared, and in page tables[b][t / 64 - n_shared] after that.
+ * Query i of sequence b sees the tokens t < lens[b] - Sq + 1 + i; query head
+ * hq reads cache head hq / (Hq / H):
+ *   s_t = (q . k_t) / sqrt(D),  p = softmax_t(s),
+ *   out[b,i,hq] = bf16_rne(sum_t p_t v_t), zero where no token is seen
+ * with k, v dequantised from the pages (code * scale), sums in 32 bits.
+ *   q        device bf16 [B x Sq x Hq x D], tokens (b, i) ldq elements apart
+ *   pages, codes4   one layer's pool
+ *   shared   device int32 [n_shared], nullable iff n_shared == 0
+ *   tables   device int32 [B x W], rows ldt apart, nullable iff W == 0: the
+ *            pages behind the shared ones (columns n_shared and up of the
+ *            kv_pages_* tables of sequences forked from one prefix)
+ *   lens     device int32 [B]
+ *   out      device bf16 [B x Sq x Hq x D]
+ *   work     device memory of at least kv_attention_3bit_paged_workspace()
+ *            bytes, 16-byte aligned, for this call alone until it has run
+ *            (nullable iff that is 0)
+ * Requires D in {64, 128, 256}, Hq a multiple of H, Sq <= 128, B <= 65535,
+ * ldq >= Hq D and a multiple of 8, q, pages, codes4, out 16-byte aligned, and
+ * finite q and scales.
+ */
+int64_t kv_attention_3bit_paged_workspace(int64_t B, int64_t Sq, int64_t Hq, int64_t H, int64_t D,
+                                          int64_t n_shared, int64_t W);
+int kv_attention_3bit_paged(const uint16_t* q, int64_t ldq, int64_t B, int64_t Sq, int64_t Hq,
+                            int64_t H, int64_t D, const uint8_t* pages, int64_t n_pages,
+                            const uint8_t* codes4, int64_t C4, const int32_t* shared,
+                            int64_t n_shared, const int32_t* tables, int64_t W, int64_t ldt,
+                            const int32_t* lens, uint16_t* out, void* work, int64_t work_bytes,
+                            int* dev_status, bitlinear_stream_t stream);
+
+/*
  * Measurement helper (not part of the method): the dense tensor-pipe rate of
  * this GPU in the MMA shapes the GEMMs issue, for roofline denominators.
  * Launches one CTA pair per two SMs (kind 0, 1) or one CTA per SM (kind 2);
@@ -274,8 +444,10 @@ int kv_attention_3bit(const uint16_t* q, int64_t B, int64_t H, int64_t D, int64_
 int bitlinear_tensor_peak(int kind, int iters, uint64_t* ns_out, int* units_out, int* dev_status,
                           bitlinear_stream_t stream);
 
-/* Synchronise the stream and read *dev_status: BITLINEAR_OK, or
- * BITLINEAR_ERR_TIMEOUT if a kernel gave up a bounded wait. */
+/* Synchronise the stream and read *dev_status: BITLINEAR_OK,
+ * BITLINEAR_ERR_TIMEOUT if a kernel gave up a bounded wait,
+ * BITLINEAR_ERR_INDEX if one met an index outside its tensors, or
+ * BITLINEAR_ERR_NO_PAGES. */
 int bitlinear_check_status(const int* dev_status, bitlinear_stream_t stream);
 
 /*
