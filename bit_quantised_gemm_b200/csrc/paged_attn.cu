@@ -23,15 +23,16 @@ namespace blt {
 namespace paged {
 
 // ----------------------------------------------------------------- operands
-// Codes are taken out of the packed stream by masks alone: a 3-bit code c at
-// bit j <= 7 of a 16-bit half, the other bits cleared, IS the fp16 subnormal
-// c 2^(j - 24). Two codes 16 bits apart (give or take what keeps both inside
-// the halves' low 10 bits) are one operand register of the m16n8k16 fp16 MMA.
-// For K the 2^j go into the queries (a power of two: exact) and the codes'
-// offset of 4 into the accumulator's start, -4 sum q: the contracted index
-// is the dimension, so both are the row's constants. For V the contracted
-// index is the token: 4 2^(j - 24) is subtracted from the operand (exact), so
-// a zero adds nothing however small the rest is, and 2^j leaves at the end.
+// A 3-bit code c at bit j <= 7 of a 16-bit half, the other bits cleared, IS the
+// fp16 subnormal c 2^(j - 24); one paired fma makes (c - 4) 2^(j - 9) of it,
+// exact and normal. Two codes 16 bits apart (give or take what keeps both in
+// the halves' low 10 bits) are so one operand register of the m16n8k16 fp16
+// MMA, for a mask, an fma and a share of a shift. The 2^j go into the queries
+// (a power of two: exact) for K, and leave at the end for V.
+// Without the fma (the subnormals as operands, the offset of 4 taken off the
+// sums) it would be 256 of 900 instructions a page less, but the MMA lines its
+// products up by the operands' exponents, where all subnormals have 2^-14:
+// with small j, 8 bits of its sums were lost.
 
 // A lane's 32 codes (96 bits) in 16 pairs, 16 codes (48 bits) in 8: the pair's
 // codes and the stream bit that lands at bit 0. Found by search: the fewest
@@ -57,33 +58,39 @@ __device__ __forceinline__ uint32_t window(const uint32_t (&X)[NW], int n) {
   return (n >> 5) + 1 < NW ? __funnelshift_r(X[n >> 5], X[(n >> 5) + 1], n & 31) : X[n >> 5] >> (n & 31);
 }
 
+// fp16 c 2^(j - 24) -> (c - 4) 2^(j - 9) in both halves
+__device__ __forceinline__ uint32_t less4(uint32_t x, int jl, int jh) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0x78007800u), "r"(0x80008000u | (jl + 8) << 10 | (jh + 8) << 26));
+  return r;
+}
+
 template <int NW>
 __device__ __forceinline__ uint32_t k_operand(const uint32_t (&X)[NW], Pair p) {
-  return window(X, p.n) & ((7u << (3 * p.lo - p.n)) | (7u << (3 * p.hi - p.n)));
+  const int jl = 3 * p.lo - p.n, jh = 3 * p.hi - p.n;
+  return less4(window(X, p.n) & ((7u << jl) | (7u << jh)), jl, jh - 16);
 }
 
 // bit of code e (0..7) in its 16-bit half as v_pair leaves it
 __host__ __device__ constexpr int v_bit(int e) { return e == 0 ? 0 : e == 1 ? 3 : e == 2 ? 6 : e == 3 ? 1 : e == 4 ? 4 : e == 5 ? 7 : e == 6 ? 2 : 5; }
 
 // Code e of 8 consecutive dimensions for 4 tokens; w[i] holds byte i of the 4
-// tokens' three bytes. r[0]: tokens 0 and 2, r[1]: tokens 1 and 3, as fp16
-// (c - 4) 2^(v_bit - 24).
+// tokens' three bytes, x[i] = w[i] >> 8. r0: tokens 0 and 2, r1: tokens 1 and 3,
+// as fp16 (c - 4) 2^(v_bit - 9).
 template <int E>
-__device__ __forceinline__ void v_operand(const uint32_t (&w)[3], uint32_t& r0, uint32_t& r1) {
-  constexpr int j = v_bit(E), B = 3 * E / 8;
+__device__ __forceinline__ void v_operand(const uint32_t (&w)[3], const uint32_t (&x)[3], uint32_t& r0, uint32_t& r1) {
+  constexpr int B = 3 * E / 8, j = v_bit(E);
   constexpr uint32_t full = 0x00070007u << j;
-  uint32_t a, b;
   if constexpr (E == 2 || E == 5) {  // the code's upper bits are the next byte's lowest
     constexpr uint32_t up = E == 2 ? 0x01000100u : 0x03000300u, low = full & 0x00FF00FFu;
-    a = (w[B] & low) | ((w[B + 1] << 8) & up);
-    b = ((w[B] >> 8) & low) | (w[B + 1] & up);
+    r0 = (w[B] & low) | ((w[B + 1] << 8) & up);
+    r1 = (x[B] & low) | (w[B + 1] & up);
   } else {
-    a = w[B] & full;
-    b = (w[B] >> 8) & full;
+    r0 = w[B] & full;
+    r1 = x[B] & full;
   }
-  constexpr uint32_t four = (0x80008000u | ((4u << j) * 0x00010001u));
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r0) : "r"(a), "r"(four));
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r1) : "r"(b), "r"(four));
+  r0 = less4(r0, j, j);
+  r1 = less4(r1, j, j);
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -138,14 +145,13 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // Its piece of segment s = (sequence, head, group) goes to slot s + w: along
 // the units either s or w grows from one piece to the next, so no two pieces
 // have one slot.
-constexpr int kStageRows4 = 4;  // 4-bit rows of a page that travel with it; pools with more are read from global memory
-constexpr int kMaxStages = 4;
+constexpr int kStageRows4 = 3;  // 4-bit rows of a page that travel with it; pools with more are read from global memory
 
 struct WalkArgs {
   AttnArgs a;
   int front;        // 1: the shared pages, all sequences' rows; 0: the own pages
   int groups;       // groups of columns of a (sequence, head)
-  int stages, stage_bytes;
+  int stage_bytes;
   int late_wait;    // an earlier kernel of this call has waited for what the call depends on
   float* parts;     // pieces
   int64_t* cum;     // [B + 1] own pages before sequence b (written)
@@ -172,11 +178,11 @@ struct Cursor {  // a unit: page j of P of segment seg = (b heads + h) groups + 
   int b, h, grp, j, P;
 };
 
-// QC: columns of a lane that are queries. 1: 4 queries, column 2 q holds query
-// q's weights rounded to fp16 and column 2 q + 1 what the rounding left (the
-// columns cost nothing); 2: 8 queries, weights rounded to fp16 (2^-11 of a
-// weight, a quarter of what the output's own rounding may take).
-template <int D, int QC, int WARPS>
+// QC: columns of a lane that are queries: 1: 4 queries a group (columns 2 q and
+// 2 q + 1 are both query q, of which one is kept: half the softmax), 2: 8.
+// The weights are rounded to fp16 for the value product: 2^-11 of a weight, a
+// quarter of what the output's own rounding may take.
+template <int D, int QC, int WARPS, int NS>
 __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_constant__ WalkArgs p) {
   constexpr int RB = row_bytes(D), NB = D / 64 * 4;  // NB: fp16 MMAs of a score
   constexpr int LD = D / 8;                          // dimensions of a lane in the value product
@@ -184,15 +190,15 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
   constexpr int COLS = 4 * QC;
   constexpr int KW = D == 64 ? 2 : 3;                // stream words of a lane's chunk
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t s_full[WARPS][kMaxStages];
-  __shared__ int s_page[WARPS][kMaxStages];
+  __shared__ uint64_t s_full[WARPS][NS];
+  __shared__ int s_page[WARPS][NS];
   __shared__ int64_t s_cum[32 * WARPS + 1];
   __shared__ int64_t s_sum[WARPS];
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
   if (lane == 0) {
-    for (int i = 0; i < p.stages; ++i) mbar_init(&s_full[warp][i], 1);
+    for (int i = 0; i < NS; ++i) mbar_init(&s_full[warp][i], 1);
     fence_mbar_init();
   }
   if (!p.late_wait) pdl_wait();
@@ -279,12 +285,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
       do { c.P = own_pages(a, ++c.b); } while (c.P == 0);  // called only while units are left
     };
 
-    const int NS = p.stages;
     uint8_t* ring = smem + static_cast<size_t>(warp) * NS * p.stage_bytes;
     const int c4_bytes = p.stage_bytes - block_bytes(D);  // 0: no 4-bit rows, or read from global memory
     // ---- the copying side: page ids 32 at a time, a lane each
     Cursor put = take;
-    int id_b = -1, id_j = -1, ids = 0, n_put = 0;
+    int id_b = -1, id_j = -1, ids = 0, n_put = 0, put_st = 0;
     auto issue = [&]() {
       if (put.b != id_b || (put.j & ~31) != id_j) {
         id_b = put.b;
@@ -293,7 +298,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
         ids = j < put.P ? (p.front ? __ldg(a.shared + j) : __ldg(a.tables + id_b * a.ldt + j)) : 0;
       }
       const int page = __shfl_sync(0xFFFFFFFFu, ids, put.j & 31);
-      const int st = n_put % NS;
+      const int st = put_st;
+      put_st = put_st + 1 == NS ? 0 : put_st + 1;
       if (lane == 0) {
         const bool good = page >= 0 && page < a.n_pages;
         s_page[warp][st] = good ? page : -1;
@@ -315,12 +321,13 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
     const int G = a.Hq / a.H;
     const int rows = (p.front ? a.B : 1) * a.Sq * G;  // of a (sequence, head)
     uint32_t parity = 0u;                             // bit per stage
+    int st = 0;
     bool ok = true;
     for (int k = 0; k < n_units && ok;) {
       // ---- a segment: its columns' queries
       const int r0 = take.grp * COLS, tok0 = p.front ? 0 : take.b * a.Sq;
       uint32_t qb[2 * NB];   // query operands: pair i of this lane's chunk of column g
-      float start[QC], kq[QC];  // -4 sum q, and what makes of (sum) x (K scale) a score in base 2
+      float kq[QC];          // what makes of (sum) x (K scale) a score in base 2
       int sees[QC];          // tokens that the lane's columns see, from the segment's first page on
       const uint16_t* qrow[QC];
       {
@@ -345,23 +352,17 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
         const int fb = min(268 - max(1, static_cast<int>(am >> 7)), 254);
         const float f = pow2_biased(fb);
         auto qf = [&](int d) { return __uint_as_float((d & 1) ? (x[d >> 1] & 0xFFFF0000u) : (x[d >> 1] << 16)) * f; };
-        float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 2 * NB; ++i) {
           const Pair pr = k_pair<D>(i);
           const int d0 = D == 64 ? 0 : 32 * (i >> 4);
           const int jl = 3 * pr.lo - pr.n, jh = 3 * pr.hi - pr.n - 16;
           qb[i] = pack_f16x2(qf(d0 + pr.lo) * (1.f / (1 << jl)), qf(d0 + pr.hi) * (1.f / (1 << jh)));
-          sum += f16lo(qb[i]) * static_cast<float>(1 << jl) + f16hi(qb[i]) * static_cast<float>(1 << jh);
         }
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-        const float st = sum * (-4.f / 16777216.f);
-        const float kr = a.qk_scale * 1.4426950408889634f * pow2_biased(min(278 - fb, 253));
+        const float kr = a.qk_scale * 1.4426950408889634f * pow2_biased(263 - fb);  // 2^(9 + 127 - fb)
 #pragma unroll
         for (int c = 0; c < QC; ++c) {
           const int src = QC == 1 ? 8 * t4 : 4 * (2 * t4 + c);  // a lane of the column's row
-          start[c] = __shfl_sync(0xFFFFFFFFu, st, src);
           kq[c] = __shfl_sync(0xFFFFFFFFu, kr, src);
           const int r = r0 + (QC == 1 ? t4 : 2 * t4 + c);
           sees[c] = 0x7FFFFFFF;  // no row: nothing is masked, nothing kept
@@ -386,10 +387,12 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
         for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
       int ve = 14;  // biased exponent that value scales are taken relative to (at least that of 2^-113)
 
-      // ---- the segment's pages
+      // ---- the segment's pages; those before page n_all are seen whole by all columns
+      int n_all = sees[0];
+      if constexpr (QC == 2) n_all = min(n_all, sees[QC - 1]);
+      n_all = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<unsigned>(n_all)) / PT);
       const int last = min(n_units - k, take.P - take.j);
       for (int e = 0; e < last; ++e, ++k) {
-        const int st = k % NS;
         const uint8_t* blk = ring + st * p.stage_bytes;
         __syncwarp();  // s_page is lane 0's
         const int page = s_page[warp][st];
@@ -398,23 +401,15 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
           ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           parity ^= 1u << st;
-          int lim[QC], most = 0;
-          bool all = true;
-#pragma unroll
-          for (int c = 0; c < QC; ++c) {
-            lim[c] = max(0, min(PT, sees[c] - (take.j + e) * PT));
-            all = all && lim[c] == PT;
-            if (qrow[c] != nullptr) most = max(most, lim[c]);
-          }
           const float* ksc = reinterpret_cast<const float*>(blk + off_ks(D));
           const float* vsc = reinterpret_cast<const float*>(blk + off_vs(D));
           // ---- scores; C row g is token 16 u + 2 g, row g + 8 the one after it
           float s[4][2][QC], vs[4][2];
-          uint32_t four = 0u;  // bit 2 u + r: the lane's token is kept at 4 bits
+          uint32_t sign = 0u;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const uint8_t* row = blk + (16 * u + 2 * g) * RB;
-            float c[4] = {start[0], start[QC - 1], start[0], start[QC - 1]};
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int h = 0; h < (D == 256 ? 2 : 1); ++h) {
               uint32_t X[2][KW];
@@ -443,15 +438,22 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
             const float2 v2 = *reinterpret_cast<const float2*>(vsc + 16 * u + 2 * g);
             vs[u][0] = v2.x;
             vs[u][1] = v2.y;
-            four |= (signbit(ks.x) ? 1u : 0u) << (2 * u) | (signbit(ks.y) ? 2u : 0u) << (2 * u);
+            sign |= __float_as_uint(ks.x) | __float_as_uint(ks.y);
 #pragma unroll
             for (int q = 0; q < QC; ++q) {
               s[u][0][q] = c[q] * ks.x;
               s[u][1][q] = c[2 + q] * ks.y;
             }
           }
-          const bool plain = __all_sync(0xFFFFFFFFu, all && four == 0u);
+          const bool plain = __all_sync(0xFFFFFFFFu, !(sign >> 31)) && take.j + e < n_all;
+          uint32_t four = 0u;  // bit 2 u + r: the lane's token is kept at 4 bits
+          int lim[QC], most = 0;
           if (!plain) {
+#pragma unroll
+            for (int c = 0; c < QC; ++c) {
+              lim[c] = max(0, min(PT, sees[c] - (take.j + e) * PT));
+              if (qrow[c] != nullptr) most = max(most, lim[c]);
+            }
             most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
             most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
 #pragma unroll
@@ -459,7 +461,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
                 const int o = 16 * u + 2 * g + r;
-                const bool is4 = (four >> (2 * u + r)) & 1u;
+                const bool is4 = signbit(ksc[o]);
+                if (is4) four |= 1u << (2 * u + r);
 #pragma unroll
                 for (int q = 0; q < QC; ++q)
                   if (is4 || o >= lim[q]) s[u][r][q] = -INFINITY;
@@ -496,7 +499,6 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
               for (int m = 0; m < NM; ++m) {
                 acc[m][q] *= f * fv;
                 acc[m][2 + q] *= f * fv;
-                if constexpr (QC == 1) { acc[m][1] *= f * fv; acc[m][3] *= f * fv; }
               }
             }
           }
@@ -515,9 +517,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
               const float p0 = ex2(fmaf(s[u][r][0], kq[0], -mr[0]));
               l_run[0] += p0;
               if constexpr (QC == 1) {
-                const float w = p0 * v;
-                b[r] = pack_f16x2(w, 0.f);
-                b[r] = pack_f16x2(w, w - f16lo(b[r]));
+                b[r] = pack_f16x2(p0 * v, 0.f);
               } else {
                 const float p1 = ex2(fmaf(s[u][r][QC - 1], kq[QC - 1], -mr[QC - 1]));
                 l_run[QC - 1] += p1;
@@ -549,12 +549,15 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
 #define BLT_V(E_)                                                                    \
             {                                                                        \
               uint32_t x0, x1, y0, y1;                                               \
-              v_operand<E_>(w[i], x0, x1);                                           \
-              v_operand<E_ + 1>(w[i], y0, y1);                                       \
+              v_operand<E_>(w[i], x, x0, x1);                                        \
+              v_operand<E_ + 1>(w[i], x, y0, y1);                                    \
               mma_f16(acc[4 * i + E_ / 2], x0, y0, x1, y1, b[0], b[1]);              \
             }
 #pragma unroll
-            for (int i = 0; i < LD / 8; ++i) { BLT_V(0) BLT_V(2) BLT_V(4) BLT_V(6) }
+            for (int i = 0; i < LD / 8; ++i) {
+              const uint32_t x[3] = {w[i][0] >> 8, w[i][1] >> 8, w[i][2] >> 8};
+              BLT_V(0) BLT_V(2) BLT_V(4) BLT_V(6)
+            }
 #undef BLT_V
           }
           // ---- the page's 4-bit tokens, one after the other: lane (g, t4) has dimensions
@@ -586,7 +589,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
                   fv = vb4 - ve > 126 ? 0.f : pow2_biased(127 - (vb4 - ve));
                   ve = vb4;
                 }
-                const float v = v4 * pow2_biased(min(268 - ve, 254)) * (1.f / 16777216.f);
+                const float v = v4 * pow2_biased(min(268 - ve, 254)) * (1.f / 512.f);
 #pragma unroll
                 for (int q = 0; q < QC; ++q) {
                   float dot = 0.f;
@@ -615,7 +618,6 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
                                     static_cast<float>(1 << v_bit(d & 7));
                     float& y = acc[d >> 1][2 * (d & 1) + q];
                     y = fmaf(pe * v, x, y * (f * fv));
-                    if constexpr (QC == 1) acc[d >> 1][2 * (d & 1) + 1] *= f * fv;
                   }
                 }
               }
@@ -624,6 +626,7 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
         }
         __syncwarp();  // all lanes are done with the stage
         if (n_put < n_units) issue();
+        st = st + 1 == NS ? 0 : st + 1;
       }
 
       // ---- the piece
@@ -643,8 +646,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
 #pragma unroll
               for (int d = 0; d < 4; ++d) {
                 const int dl = 4 * c + d;
-                x[d] = (QC == 1 ? acc[dl >> 1][2 * (dl & 1)] + acc[dl >> 1][2 * (dl & 1) + 1] : acc[dl >> 1][2 * (dl & 1) + q]) *
-                       (1024.f / static_cast<float>(1 << v_bit(dl & 7))) * pow2_biased(ve);  // 2^(24 - 14 + ve - 127)
+                x[d] = acc[dl >> 1][2 * (dl & 1) + q] * (1.f / static_cast<float>(32 << v_bit(dl & 7))) *
+                       pow2_biased(ve);  // 2^(9 - 14 + ve - 127 - v_bit)
               }
               dst[c] = make_float4(x[0], x[1], x[2], x[3]);
             }
@@ -755,7 +758,8 @@ struct Plan {
   int64_t off_front, off_cum, bytes;
 };
 
-constexpr int walk_warps(int D) { return D == 256 ? 8 : 12; }
+constexpr int walk_warps(int D) { return D == 256 ? 8 : 16; }
+constexpr int walk_stages(int D) { return D == 64 ? 3 : 2; }
 
 static Plan::Walk plan_walk(int64_t D, int64_t rows, int64_t segs_per_group, int64_t max_units_per_group, bool any) {
   Plan::Walk w{};
@@ -801,8 +805,7 @@ template <int D, int QC>
 static cudaError_t launch_walk(const AttnArgs& a, const Plan::Walk& w, bool front, bool behind, float* parts, int64_t* cum,
                                cudaStream_t s) {
   constexpr int kWarps = walk_warps(D);
-  auto kern = walk_kernel<D, QC, kWarps>;
-  const int limit = 220 * 1024;
+  auto kern = walk_kernel<D, QC, kWarps, walk_stages(D)>;
   WalkArgs p{};
   p.a = a;
   p.front = front;
@@ -811,10 +814,8 @@ static cudaError_t launch_walk(const AttnArgs& a, const Plan::Walk& w, bool fron
   p.parts = parts;
   p.cum = cum;
   p.stage_bytes = block_bytes(D) + (a.C4 <= kStageRows4 ? a.C4 * D : 0);
-  p.stages = limit / (kWarps * p.stage_bytes);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const int smem = p.stages * kWarps * p.stage_bytes;
-  cudaError_t e = set_smem_limit(kern, limit);
+  const int smem = walk_stages(D) * kWarps * p.stage_bytes;
+  cudaError_t e = set_smem_limit(kern, smem);
   if (e != cudaSuccess) return e;
   const dim3 grid(static_cast<unsigned>(w.grid));
   if (behind) return launch_behind(kern, grid, dim3(32 * kWarps), smem, s, p);
