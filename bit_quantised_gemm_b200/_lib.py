@@ -1,4 +1,5 @@
-"""ctypes binding of libbitlinear.so: argument marshalling only.
+"""ctypes binding of libbitlinear.so: argument marshalling only (that of the
+paged-cache calls is compiled: csrc/bind.cpp).
 
 Every computation happens in the CUDA library; this module passes device
 pointers, sizes and the current CUDA stream, allocates outputs with torch,
@@ -477,74 +478,22 @@ def kv_attention_3bit(q: torch.Tensor, k_store, v_store, keep4_pos: torch.Tensor
 
 
 # ------------------------------------------------------- paged 3-bit cache
-def _paged_call(dev, stream, status, fn, *args):
-    """Call a paged-cache function on `dev`, whichever device is current."""
-    if status is None:
-        status = status_buffer(dev)
-    if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    elif stream.device != dev:
-        raise ValueError(f"a stream of {stream.device} for tensors of {dev}")
-    if torch.cuda.current_device() == dev.index:
-        return fn(*args, status.data_ptr(), stream.cuda_stream)
-    with torch.cuda.device(dev):
-        return fn(*args, status.data_ptr(), stream.cuda_stream)
+_bind = None
 
 
-def _paged_empty(stream, shape, dtype, dev):
-    """Memory that the call's stream owns: it may go back as soon as the call's work is queued."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
-
-
-def _same_device(dev, *named):
-    if dev.type != "cuda":
-        raise ValueError("expected a CUDA tensor")
-    for name, t in named:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, expected {dev}")
-
-
-def _ints(t, name, dim=1, size=None):
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name}: dtype {t.dtype}, expected torch.int32")
-    if t.dim() != dim or not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous and {dim}-D")
-    if size is not None and t.numel() != size:
-        raise ValueError(f"{name}: {t.numel()} values, expected {size}")
-
-
-_BLOCK_D = {PAGE_TOKENS * (3 * D // 4 + 8): D for D in (64, 128, 256)}
-
-
-def _pool(pages, codes4, dim):
-    """(H, D, rows4) of a pool [..., n_pages x H x block] and its 4-bit rows."""
-    if pages.dtype != torch.uint8 or pages.dim() not in dim or not pages.is_contiguous():
-        raise ValueError(f"pages: must be a contiguous uint8 tensor [{'L x ' if 4 in dim else ''}n_pages x H x block]")
-    H, block = pages.shape[-2:]
-    D = _BLOCK_D.get(block)
-    if D is None:
-        raise ValueError(f"pages: blocks of {block} bytes, expected kv_page_block_bytes(D)")
-    if codes4 is None:
-        return H, D, 0
-    if codes4.dtype != torch.uint8 or not codes4.is_contiguous():
-        raise ValueError("codes4: must be a contiguous uint8 tensor")
-    if codes4.dim() != pages.dim() + 1 or codes4.shape[:-2] != pages.shape[:-1] or codes4.shape[-1] != D:
-        raise ValueError(f"codes4: shape {tuple(codes4.shape)}, expected {tuple(pages.shape[:-1])} + (rows4, {D})")
-    return H, D, codes4.shape[-2]
-
-
-def _tables(tables, lens, refs):
-    """(R, W, ldt) of the sequences' tables."""
-    if tables.dtype != torch.int32 or tables.dim() != 2 or (tables.shape[1] > 1 and tables.stride(1) != 1):
-        raise ValueError("tables: must be an int32 tensor [R x W] with contiguous rows")
-    R, W = tables.shape
-    _ints(lens, "lens", size=R)
-    if refs is not None:
-        _ints(refs, "refs")
-    return R, W, tables.stride(0) if R > 1 else max(W, 1)
+def _paged():
+    """The module that marshals the calls below (csrc/bind.cpp), loaded on first use."""
+    global _bind
+    if _bind is None:
+        try:
+            from . import _bind as m
+        except ImportError as e:
+            raise RuntimeError(f"{_HERE}/_bind.so cannot be loaded ({e}): build it with "
+                               "`python -m bit_quantised_gemm_b200.build`") from e
+        names = [n for n in _SIGS if n.startswith("kv_")]
+        m.setup(_check, status_buffer, {n: _c.cast(getattr(lib(), n), _P).value for n in names})
+        _bind = m
+    return _bind
 
 
 def kv_page_block_bytes(D: int) -> int:
@@ -568,53 +517,20 @@ def kv_append_3bit(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, pages:
     """Quantise tokens k, v [n x H x D] (bf16; heads contiguous, any token stride)
     into the slots (page * 64 + place; negative: left out) of one layer's pool.
     row4[i] >= 0 keeps token i at 4 bits, in that row of its page in codes4."""
-    H, D, C4 = _pool(pages, codes4, (3,))
-    for name, t in (("k", k), ("v", v)):
-        _need(t, name, _BF16_LIKE, 3)
-        if tuple(t.shape[1:]) != (H, D) or (t.numel() and (t.stride(2) != 1 or (H > 1 and t.stride(1) != D))):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, strides {t.stride()}, expected [n x {H} x {D}] "
-                             "with contiguous heads")
-    n = k.shape[0]
-    if v.shape[0] != n:
-        raise ValueError(f"v: {v.shape[0]} tokens, k has {n}")
-    _ints(slots, "slots", size=n)
-    if row4 is not None:
-        _ints(row4, "row4", size=n)
-    dev = pages.device
-    _same_device(dev, ("k", k), ("v", v), ("slots", slots), ("row4", row4), ("codes4", codes4), ("status", status))
-    ldk, ldv = (k.stride(0), v.stride(0)) if n > 1 else (H * D, H * D)
-    _check(_paged_call(dev, stream, status, lib().kv_append_3bit, _ptr(k), ldk, _ptr(v), ldv, n, H, D, _ptr(slots),
-                       _ptr(row4), _ptr(pages), pages.shape[0], _ptr(codes4), C4))
-
-
-def _layers(pages, codes4):
-    """(page bytes, 4-bit bytes a page, L, n_pages) of a pool of one or more layers."""
-    H, D, C4 = _pool(pages, codes4, (3, 4))
-    return H * pages.shape[-1], H * C4 * D, pages.shape[0] if pages.dim() == 4 else 1, pages.shape[-3]
+    _paged().append(k, v, slots, pages, row4, codes4, status, stream)
 
 
 def kv_pages_copy(pages: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, codes4: torch.Tensor | None = None,
                   status=None, stream=None):
     """Copy page src[i] onto page dst[i] in every layer of a pool
     [L x n_pages x H x block] (or of one layer). Pairs of negative pages are left out."""
-    pb, pb4, L, n_pages = _layers(pages, codes4)
-    _ints(src, "src")
-    _ints(dst, "dst", size=src.numel())
-    _same_device(pages.device, ("src", src), ("dst", dst), ("codes4", codes4), ("status", status))
-    _check(_paged_call(pages.device, stream, status, lib().kv_pages_copy, _ptr(pages), pb, _ptr(codes4), pb4, L,
-                       n_pages, _ptr(src), _ptr(dst), src.numel()))
+    _paged().copy(pages, src, dst, codes4, status, stream)
 
 
 def kv_pages_fork(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, parents: torch.Tensor,
                   children: torch.Tensor, status=None, stream=None):
     """Row children[i] becomes the sequence of row parents[i], on the same pages."""
-    R, W, ldt = _tables(tables, lens, refs)
-    _ints(parents, "parents")
-    _ints(children, "children", size=parents.numel())
-    _same_device(tables.device, ("lens", lens), ("refs", refs), ("parents", parents), ("children", children),
-                 ("status", status))
-    _check(_paged_call(tables.device, stream, status, lib().kv_pages_fork, _ptr(tables), R, W, ldt, _ptr(lens),
-                       _ptr(refs), refs.numel(), _ptr(parents), _ptr(children), parents.numel()))
+    _paged().fork(tables, lens, refs, parents, children, status, stream)
 
 
 def kv_pages_grow(pages: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
@@ -623,58 +539,20 @@ def kv_pages_grow(pages: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor,
     """Make room for n_new[i] <= max_new more tokens of row rows[i] (a shared,
     partly filled last page is copied first) and return their slots
     [n x max_new], -1 behind a row's last one."""
-    pb, pb4, L, n_pages = _layers(pages, codes4)
-    R, W, ldt = _tables(tables, lens, refs)
-    _ints(refs, "refs", size=n_pages)
-    _ints(rows, "rows")
-    n = rows.numel()
-    _ints(n_new, "n_new", size=n)
-    if max_new < 0:
-        raise ValueError(f"max_new = {max_new}")
-    dev = pages.device
-    _same_device(dev, ("tables", tables), ("lens", lens), ("refs", refs), ("rows", rows), ("n_new", n_new),
-                 ("codes4", codes4), ("status", status))
-    slots = _paged_empty(stream, (n, max_new), torch.int32, dev)
-    work = _paged_empty(stream, (2 * n,), torch.int32, dev)
-    _check(_paged_call(dev, stream, status, lib().kv_pages_grow, _ptr(pages), pb, _ptr(codes4), pb4, L, n_pages,
-                       _ptr(tables), R, W, ldt, _ptr(lens), _ptr(refs), _ptr(rows), _ptr(n_new), n, max_new,
-                       _ptr(slots), _ptr(work)))
-    return slots
+    return _paged().grow(pages, tables, lens, refs, rows, n_new, max_new, codes4, status, stream)
 
 
 def kv_pages_free(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, rows: torch.Tensor,
                   keep: torch.Tensor | None = None, status=None, stream=None):
     """Row rows[i] keeps its first keep[i] tokens (none without keep); the pages behind them lose its reference."""
-    R, W, ldt = _tables(tables, lens, refs)
-    _ints(rows, "rows")
-    if keep is not None:
-        _ints(keep, "keep", size=rows.numel())
-    _same_device(tables.device, ("lens", lens), ("refs", refs), ("rows", rows), ("keep", keep), ("status", status))
-    _check(_paged_call(tables.device, stream, status, lib().kv_pages_free, _ptr(tables), R, W, ldt, _ptr(lens),
-                       _ptr(refs), refs.numel(), _ptr(rows), _ptr(keep), rows.numel()))
+    _paged().release(tables, lens, refs, rows, keep, status, stream)
 
 
 def kv_pages_compact(pages: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
                      codes4: torch.Tensor | None = None, status=None, stream=None) -> torch.Tensor:
     """Move the pages in use to the front of the pool, in every layer and table;
     returns their number (int32 [1] on the device)."""
-    pb, pb4, L, n_pages = _layers(pages, codes4)
-    R, W, ldt = _tables(tables, lens, refs)
-    _ints(refs, "refs", size=n_pages)
-    dev = pages.device
-    _same_device(dev, ("tables", tables), ("lens", lens), ("refs", refs), ("codes4", codes4), ("status", status))
-    n_live = _paged_empty(stream, (1,), torch.int32, dev)
-    work = _paged_empty(stream, (2 * n_pages + 3,), torch.int32, dev)
-    _check(_paged_call(dev, stream, status, lib().kv_pages_compact, _ptr(pages), pb, _ptr(codes4), pb4, L, n_pages,
-                       _ptr(tables), R, W, ldt, _ptr(lens), _ptr(refs), _ptr(n_live), _ptr(work)))
-    return n_live
-
-
-def _paged_workspace_bytes(B, Sq, Hq, H, D, n_shared, W):
-    n = lib().kv_attention_3bit_paged_workspace(B, Sq, Hq, H, D, n_shared, W)
-    if n < 0:
-        _check(n)
-    return n
+    return _paged().compact(pages, tables, lens, refs, codes4, status, stream)
 
 
 def kv_attention_3bit_paged_workspace(q: torch.Tensor, pages: torch.Tensor, tables: torch.Tensor,
@@ -684,7 +562,10 @@ def kv_attention_3bit_paged_workspace(q: torch.Tensor, pages: torch.Tensor, tabl
     if q.dim() != 4:
         raise ValueError("q must be a [B x Sq x Hq x D] tensor")
     B, Sq, Hq, D = q.shape
-    n = _paged_workspace_bytes(B, Sq, Hq, pages.shape[-2], D, 0 if shared is None else shared.numel(), tables.shape[1])
+    n = lib().kv_attention_3bit_paged_workspace(B, Sq, Hq, pages.shape[-2], D, 0 if shared is None else shared.numel(),
+                                                tables.shape[1])
+    if n < 0:
+        _check(n)
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
 
@@ -695,39 +576,7 @@ def kv_attention_3bit_paged(q: torch.Tensor, pages: torch.Tensor, tables: torch.
     stride) over one layer's pool. Sequence b is the pages `shared`, then
     tables[b]; lens[b] counts all its tokens, the last Sq of them the queries'
     own: query i sees the tokens before lens[b] - Sq + 1 + i."""
-    H, D, C4 = _pool(pages, codes4, (3,))
-    _need(q, "q", _BF16_LIKE, 4)
-    B, Sq, Hq, Dq = q.shape
-    if Dq != D:
-        raise ValueError(f"q: head dimension {Dq}, the pages hold {D}")
-    st = q.stride()
-    if q.numel() and (st[3] != 1 or (Hq > 1 and st[2] != D) or (B > 1 and Sq > 1 and st[0] != Sq * st[1])):
-        raise ValueError(f"q: strides {st}, expected contiguous heads and evenly spaced tokens")
-    ldq = st[1] if Sq > 1 else st[0] if B > 1 else Hq * D
-    R, W, ldt = _tables(tables, lens, None)
-    if R != B:
-        raise ValueError(f"tables: {R} rows for {B} sequences")
-    n_shared = 0
-    if shared is not None:
-        _ints(shared, "shared")
-        n_shared = shared.numel()
-    if out is not None:
-        _need(out, "out", _BF16_LIKE, 4, contiguous=True)
-        if out.shape != q.shape:
-            raise ValueError(f"out: shape {tuple(out.shape)}, expected {tuple(q.shape)}")
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace: must be contiguous")
-    dev = q.device
-    _same_device(dev, ("pages", pages), ("tables", tables), ("lens", lens), ("shared", shared), ("codes4", codes4),
-                 ("out", out), ("workspace", workspace), ("status", status))
-    if out is None:
-        out = _paged_empty(stream, q.shape, torch.bfloat16, dev)
-    if workspace is None:
-        workspace = _paged_empty(stream, (_paged_workspace_bytes(B, Sq, Hq, H, D, n_shared, W),), torch.uint8, dev)
-    _check(_paged_call(dev, stream, status, lib().kv_attention_3bit_paged, _ptr(q), ldq, B, Sq, Hq, H, D, _ptr(pages),
-                       pages.shape[0], _ptr(codes4), C4, _ptr(shared), n_shared, _ptr(tables), W, ldt, _ptr(lens),
-                       _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size()))
-    return out
+    return _paged().attention(q, pages, tables, lens, shared, codes4, out, workspace, status, stream)
 
 
 def tensor_peak(kind: int, iters: int = 4096, status=None, stream=None) -> dict:

@@ -1,4 +1,5 @@
-"""Build the CUDA library (libbitlinear.so) in-tree with nvcc for sm_100a.
+"""Build the CUDA library (libbitlinear.so) in-tree with nvcc for sm_100a, and the
+paged-cache calls' binding (_bind.so) with the host compiler.
 
     python -m bit_quantised_gemm_b200.build [--verbose]
 
@@ -17,6 +18,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libbitlinear.so")
+BIND = os.path.join(PKG, "_bind.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "gemv.cu", "gemv_mma.cu", "gemv_dp4a.cu", "attn.cu", "paged.cu", "paged_attn.cu",
            "peak.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -57,6 +59,21 @@ def build(verbose: bool = False, force: bool = False) -> str:
         subprocess.run(cmd, check=True)
     if force or _stale(LIB, objs):
         cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", LIB, *objs]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+    src = os.path.join(CSRC, "bind.cpp")
+    if force or _stale(BIND, [src, os.path.join(ROOT, "include", "bitlinear.h")]):
+        import sysconfig
+
+        import torch
+        t = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(nvcc))
+        # the system's g++, whose C++ runtime is torch's: a statically linked one breaks exceptions
+        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+               "-I", os.path.join(t, "include"), "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+               "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], src, "-o", BIND,
+               "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
