@@ -55,8 +55,11 @@ __host__ __device__ constexpr int piece_floats(int D, int cols) { return cols * 
 
 // warps that have units (each one at least), the first unit of warp w, and the warp that has unit u
 __device__ __forceinline__ int64_t walkers(int64_t U, int64_t NW) { return U < NW ? U : NW; }
-__device__ __forceinline__ int64_t first_unit(int64_t U, int64_t w, int64_t NW) { return U * w / NW; }
-__device__ __forceinline__ int64_t warp_of(int64_t U, int64_t u, int64_t NW) { return ((u + 1) * NW - 1) / U; }
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {  // of numbers that are not negative
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+__device__ __forceinline__ int64_t first_unit(int64_t U, int64_t w, int64_t NW) { return quot(U * w, NW); }
+__device__ __forceinline__ int64_t warp_of(int64_t U, int64_t u, int64_t NW) { return quot((u + 1) * NW - 1, U); }
 
 struct Cursor {  // a unit: page j of P of segment seg = (b heads + h) groups + group
   int b, h, grp, j, P;
@@ -125,15 +128,15 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
     Cursor take;
     int64_t seg;
     if (p.front) {
-      seg = u0 / a.n_shared;
+      seg = quot(u0, a.n_shared);
       take.b = 0;
       take.P = a.n_shared;
       take.j = static_cast<int>(u0 - seg * a.n_shared);
-      take.h = static_cast<int>(seg / p.groups);
+      take.h = static_cast<int>(quot(seg, p.groups));
       take.grp = static_cast<int>(seg - static_cast<int64_t>(take.h) * p.groups);
     } else {
       const int64_t hg = static_cast<int64_t>(a.H) * p.groups;
-      const int64_t pg = u0 / hg;
+      const int64_t pg = quot(u0, hg);
       int lo = 0, hi = 32 * WARPS - 1;  // the last chunk that begins at or before pg
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -142,11 +145,11 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
       int64_t c = s_cum[lo];
       int b = lo * chunk, P = own_pages(a, b);
       while (c + P <= pg) { c += P; P = own_pages(a, ++b); }
-      const int64_t v = u0 - c * hg, s = v / P;
+      const int64_t v = u0 - c * hg, s = quot(v, P);
       take.b = b;
       take.P = P;
       take.j = static_cast<int>(v - s * P);
-      take.h = static_cast<int>(s / p.groups);
+      take.h = static_cast<int>(quot(s, p.groups));
       take.grp = static_cast<int>(s - static_cast<int64_t>(take.h) * p.groups);
       seg = static_cast<int64_t>(b) * hg + s;
     }
@@ -220,7 +223,8 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
         st = st + 1 == NS ? 0 : st + 1;
       }
 
-      if (ok) pg.finish(out);
+      // a whole segment, and nothing in front of it: the rows are done
+      if (ok) pg.finish(a, sg, out, !p.front && a.n_shared == 0 && take.j == 0 && last == take.P);
       // the next segment
       if (ok && k < n_units) {
         take.j = take.P - 1;
@@ -239,8 +243,9 @@ __global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_consta
 }
 
 // --------------------------------------------------------------------- join
-// A block a row (query, head): its warps take the row's pieces in turn, a lane
-// D / 32 dimensions, then the warps' sums meet.
+// WPR warps a row (query, head), D / 32 dimensions a lane; lane i reads the
+// maximum and sum of the warp's i-th piece, then all pieces' values come with
+// their factors known, so that their loads do not wait for one another.
 struct JoinArgs {
   AttnArgs a;
   const float* own;      // null: no own pages
@@ -250,32 +255,61 @@ struct JoinArgs {
   int own_groups, front_groups, own_cols, front_cols;
 };
 
-template <int D>
+template <int D, int WPR>
 __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinArgs p) {
-  constexpr int DL = D / 32;
-  __shared__ float s_m[4], s_l[4], s_o[4][D];
+  constexpr int DL = D / 32, VL = DL < 4 ? DL : 4;  // VL: dimensions side by side
+  __shared__ float s_m[4], s_l[4], s_o[WPR == 1 ? 1 : 4][D];
   const AttnArgs& a = p.a;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_wait();
   pdl_trigger();
-  const int tok = blockIdx.y, hq = blockIdx.x;
-  const int G = a.Hq / a.H, h = hq / G, gg = hq % G;
+  const int row = blockIdx.x * (4 / WPR) + (WPR == 1 ? warp : 0);
+  if (row >= a.B * a.Sq * a.Hq) return;
+  const int sub = WPR == 1 ? 0 : warp;
+  const int tok = row / a.Hq, hq = row - tok * a.Hq;
+  const int G = a.Hq / a.H, h = hq / G, gg = hq - h * G;
   float m = -INFINITY, l = 0.f, o[DL];
 #pragma unroll
   for (int i = 0; i < DL; ++i) o[i] = 0.f;
   auto add = [&](const float* base, int cols, int col, int64_t first, int64_t n) {
-    for (int64_t i = warp; i < n; i += 4) {
-      const float* x = base + (first + i) * piece_floats(D, cols);
-      const float pm = x[cols * D + col], pl = x[cols * D + cols + col];
-      float v[DL];
+    const int64_t size = piece_floats(D, cols);
+    for (int64_t i0 = sub; i0 < n; i0 += 32 * WPR) {
+      float pm = -INFINITY, pl = 0.f;
+      if (i0 + WPR * lane < n) {
+        const float* x = base + (first + i0 + WPR * lane) * size + cols * D + col;
+        pm = x[0];
+        pl = x[cols];
+      }
+      float mn = fmaxf(m, pm);
 #pragma unroll
-      for (int d = 0; d < DL; ++d) v[d] = x[col * D + lane + 32 * d];
-      const float mn = fmaxf(m, pm);
-      const float f0 = mn == -INFINITY ? 0.f : ex2(m - mn), f1 = mn == -INFINITY ? 0.f : ex2(pm - mn);
+      for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xFFFFFFFFu, mn, x));
+      const float f0 = m == -INFINITY ? 0.f : ex2(m - mn), f = pm == -INFINITY ? 0.f : ex2(pm - mn);
       m = mn;
-      l = l * f0 + pl * f1;
+      pl *= f;
 #pragma unroll
-      for (int d = 0; d < DL; ++d) o[d] = o[d] * f0 + v[d] * f1;
+      for (int x = 16; x > 0; x >>= 1) pl += __shfl_xor_sync(0xFFFFFFFFu, pl, x);
+      l = fmaf(l, f0, pl);
+#pragma unroll
+      for (int d = 0; d < DL; ++d) o[d] *= f0;
+      const int cnt = static_cast<int>(min(static_cast<int64_t>(32), (n - i0 + WPR - 1) / WPR));
+      const float* v = base + (first + i0) * size + col * D + lane * VL;
+#pragma unroll 4
+      for (int j = 0; j < cnt; ++j) {
+        const float fj = __shfl_sync(0xFFFFFFFFu, f, j);
+#pragma unroll
+        for (int c = 0; c < DL / VL; ++c) {
+          float y[VL];
+          if constexpr (VL == 4) {
+            const float4 t = *reinterpret_cast<const float4*>(v + j * WPR * size + 128 * c);
+            y[0] = t.x; y[1] = t.y; y[2] = t.z; y[3] = t.w;
+          } else {
+            const float2 t = *reinterpret_cast<const float2*>(v + j * WPR * size);
+            y[0] = t.x; y[1] = t.y;
+          }
+#pragma unroll
+          for (int e = 0; e < VL; ++e) o[VL * c + e] = fmaf(fj, y[e], o[VL * c + e]);
+        }
+      }
     }
   };
   if (p.own != nullptr) {
@@ -284,6 +318,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinA
     if (P > 0) {
       const int64_t U = p.cum[a.B] * hg, u = c * hg + (static_cast<int64_t>(h) * p.own_groups + grp) * P;
       const int64_t nw = walkers(U, p.own_nw), w0 = warp_of(U, u, nw), w1 = warp_of(U, u + P - 1, nw);
+      if (p.front == nullptr && w0 == w1) return;  // the walk has written the row
       add(p.own, p.own_cols, r % p.own_cols, static_cast<int64_t>(b) * hg + static_cast<int64_t>(h) * p.own_groups + grp + w0, w1 - w0 + 1);
     }
   }
@@ -293,24 +328,38 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinA
     const int64_t nw = walkers(U, p.front_nw), w0 = warp_of(U, seg * a.n_shared, nw), w1 = warp_of(U, (seg + 1) * a.n_shared - 1, nw);
     add(p.front, p.front_cols, r % p.front_cols, seg + w0, w1 - w0 + 1);
   }
-  if (p.own == nullptr && p.front == nullptr && threadIdx.x == 0 && __ldg(a.lens + tok / a.Sq) != 0)
+  if (p.own == nullptr && p.front == nullptr && lane == 0 && __ldg(a.lens + tok / a.Sq) != 0)
     report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);  // no page at all
-  if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
+  uint16_t* out = a.out + static_cast<int64_t>(row) * D;
+  if constexpr (WPR == 1) {
+    const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int d = 0; d < DL; ++d) s_o[warp][lane + 32 * d] = o[d];
-  __syncthreads();
-  const float M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-  float f[4], L = 0.f;
+    for (int c = 0; c < DL / VL; ++c) {
+      uint32_t x[VL / 2];
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    f[w] = s_m[w] == -INFINITY ? 0.f : ex2(s_m[w] - M);
-    L = fmaf(f[w], s_l[w], L);
-  }
-  for (int d = threadIdx.x; d < D; d += 128) {
-    float O = 0.f;
+      for (int e = 0; e < VL / 2; ++e) x[e] = pack_bf16x2(o[VL * c + 2 * e] * inv, o[VL * c + 2 * e + 1] * inv);
+      if constexpr (VL == 4) reinterpret_cast<uint2*>(out + 128 * c)[lane] = make_uint2(x[0], x[1]);
+      else reinterpret_cast<uint32_t*>(out)[lane] = x[0];
+    }
+  } else {
+    if (lane == 0) { s_m[warp] = m; s_l[warp] = l; }
 #pragma unroll
-    for (int w = 0; w < 4; ++w) O = fmaf(f[w], s_o[w][d], O);
-    a.out[(static_cast<int64_t>(tok) * a.Hq + hq) * D + d] = __bfloat16_as_ushort(__float2bfloat16_rn(L > 0.f ? O / L : 0.f));
+    for (int d = 0; d < DL; ++d) s_o[warp][VL * lane + 128 * (d / VL) + d % VL] = o[d];
+    __syncthreads();
+    const float M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    float f[4], L = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      f[w] = s_m[w] == -INFINITY ? 0.f : ex2(s_m[w] - M);
+      L = fmaf(f[w], s_l[w], L);
+    }
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    for (int d = threadIdx.x; d < D; d += 128) {
+      float O = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) O = fmaf(f[w], s_o[w][d], O);
+      out[d] = __bfloat16_as_ushort(__float2bfloat16_rn(O * inv));
+    }
   }
 }
 
@@ -419,9 +468,16 @@ static cudaError_t launch_all(const AttnArgs& a, cudaStream_t s) {
     e = walk(pl.own, false, parts);
   }
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(a.Hq), static_cast<unsigned>(a.B * a.Sq));
-  if (behind) return launch_behind(join_kernel<D>, grid, dim3(128), 0, s, j);
-  return launch_kernel(join_kernel<D>, grid, dim3(128), 0, s, 0u, j);
+  // A warp a row while a row has few pieces (64 sequences of up to 4096 tokens, 2 pieces: 4 us against
+  // 7.7 with a block a row); four where one sequence's pages went to many warps.
+  const int64_t rows = static_cast<int64_t>(a.B) * a.Sq * a.Hq;
+  const int64_t pieces = (j.own ? pl.own.nw / (static_cast<int64_t>(a.B) * a.H * pl.own.groups) + 1 : 0) +
+                         (j.front ? pl.front.nw / (static_cast<int64_t>(a.H) * pl.front.groups) + 1 : 0);
+  const bool wide = pieces > 16;
+  const dim3 grid(static_cast<unsigned>(wide ? rows : (rows + 3) / 4));
+  auto join = wide ? join_kernel<D, 4> : join_kernel<D, 1>;
+  if (behind) return launch_behind(join, grid, dim3(128), 0, s, j);
+  return launch_kernel(join, grid, dim3(128), 0, s, 0u, j);
 }
 
 }  // namespace paged

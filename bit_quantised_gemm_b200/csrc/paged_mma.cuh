@@ -32,6 +32,10 @@ __device__ __forceinline__ const uint16_t* query_row(const AttnArgs& a, const Se
   return a.q + (s.tok0 + r / s.G) * a.ldq + static_cast<int64_t>(s.h * s.G + r % s.G) * a.D;
 }
 
+__device__ __forceinline__ uint16_t* output_row(const AttnArgs& a, const Segment& s, int r) {
+  return a.out + (static_cast<int64_t>(s.tok0 + r / s.G) * a.Hq + s.h * s.G + r % s.G) * a.D;
+}
+
 // Tokens that row r sees, from the segment's first page on; a row that is none: all, so that nothing is masked for it.
 __device__ __forceinline__ int row_sees(const AttnArgs& a, const Segment& s, int r) {
   if (r >= s.rows) return 0x7FFFFFFF;
@@ -442,7 +446,8 @@ struct F16Page {
     }
   }
 
-  __device__ __forceinline__ void finish(float* out) {
+  // The piece, or the rows themselves.
+  __device__ __forceinline__ void finish(const AttnArgs& a, const Segment& sg, float* out, bool whole) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
 #pragma unroll
     for (int q = 0; q < QC; ++q) {
@@ -450,23 +455,24 @@ struct F16Page {
       float l = l_run[q];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-      if (qrow[q] != nullptr) {
-        float4* dst = reinterpret_cast<float4*>(out + col * D + LD * g);
+      if (qrow[q] == nullptr) continue;
+      const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
+      uint16_t* row = output_row(a, sg, sg.r0 + col) + LD * g;
 #pragma unroll
-        for (int c = 0; c < LD / 4; ++c) {
-          float x[4];
+      for (int c = 0; c < LD / 4; ++c) {
+        float x[4];
 #pragma unroll
-          for (int d = 0; d < 4; ++d) {
-            const int dl = 4 * c + d;
-            x[d] = acc[dl >> 1][2 * (dl & 1) + q] * (1.f / static_cast<float>(32 << v_bit(dl & 7))) *
-                   pow2_biased(ve);  // 2^(9 - 14 + ve - 127 - v_bit)
-          }
-          dst[c] = make_float4(x[0], x[1], x[2], x[3]);
+        for (int d = 0; d < 4; ++d) {
+          const int dl = 4 * c + d;
+          x[d] = acc[dl >> 1][2 * (dl & 1) + q] * (1.f / static_cast<float>(32 << v_bit(dl & 7))) *
+                 pow2_biased(ve) * inv;  // 2^(9 - 14 + ve - 127 - v_bit)
         }
-        if (g == 0) {
-          out[COLS * D + col] = m_run[q];
-          out[COLS * D + COLS + col] = l;
-        }
+        if (whole) reinterpret_cast<uint2*>(row)[c] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+        else reinterpret_cast<float4*>(out + col * D + LD * g)[c] = make_float4(x[0], x[1], x[2], x[3]);
+      }
+      if (!whole && g == 0) {
+        out[COLS * D + col] = m_run[q];
+        out[COLS * D + COLS + col] = l;
       }
     }
   }
@@ -626,7 +632,8 @@ struct I8Page {
 
   // The sums so far go to the piece, which is then relative to 2^m_new: a lane of
   // the two that have a row's digits writes half of their dimensions.
-  __device__ __forceinline__ void flush(float m_new) {
+  // With `row`, the row itself: what there is, times inv.
+  __device__ __forceinline__ void flush(float m_new, uint16_t* row = nullptr, float inv = 1.f) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
     const float f = m_ref == -INFINITY ? 0.f : ex2(m_ref - m_new);
     const float us = pow2_biased(127 - 16) * pow2_biased(max(w_exp - 15, 1)) * f;  // 2^(w_exp - 158) in two steps
@@ -670,7 +677,11 @@ struct I8Page {
             x[0] = fmaf(old.x, f, x[0]); x[1] = fmaf(old.y, f, x[1]);
             x[2] = fmaf(old.z, f, x[2]); x[3] = fmaf(old.w, f, x[3]);
           }
-          *d4 = make_float4(x[0], x[1], x[2], x[3]);
+          if (row != nullptr)
+            reinterpret_cast<uint2*>(row + LD * g + (t4 & 1) * (LD / 2))[q] =
+                make_uint2(pack_bf16x2(x[0] * inv, x[1] * inv), pack_bf16x2(x[2] * inv, x[3] * inv));
+          else
+            *d4 = make_float4(x[0], x[1], x[2], x[3]);
         }
       }
     }
@@ -904,13 +915,14 @@ struct I8Page {
     }
   }
 
-  __device__ __forceinline__ void finish(float* out) {
+  __device__ __forceinline__ void finish(const AttnArgs& a, const Segment& sg, float* out, bool whole) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
-    flush(m_ref);
     float l = l_run;
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-    if (g == 0 && (t4 & 1) == 0 && qrow != nullptr) {
+    uint16_t* row = whole && qrow != nullptr ? output_row(a, sg, sg.r0 + (t4 >> 1)) : nullptr;
+    flush(m_ref, row, l > 0.f ? 1.f / l : 0.f);
+    if (g == 0 && (t4 & 1) == 0 && qrow != nullptr && !whole) {
       out[COLS * D + (t4 >> 1)] = m_ref;
       out[COLS * D + COLS + (t4 >> 1)] = l;
     }
