@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libbitlinear.so")
 BIND = os.path.join(PKG, "_bind.so")
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "gemv.cu", "gemv_mma.cu", "gemv_dp4a.cu", "attn.cu", "paged.cu", "paged_attn.cu",
-           "peak.cu"]
+           "paged_front.cu", "peak.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 

@@ -17,17 +17,12 @@
 
 #include "launch.h"
 #include "paged.cuh"
+#include "paged_front.cuh"
 #include "paged_mma.cuh"
 #include "ptx.cuh"
 
 namespace blt {
 namespace paged {
-
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
-  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-               "l"(src), "r"(bytes), "r"(smem_u32(bar))
-               : "memory");
-}
 
 // --------------------------------------------------------------------- walk
 // A unit is (page, cache head, group of columns). The units of one (sequence,
@@ -39,7 +34,6 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
 // Its piece of segment s = (sequence, head, group) goes to slot s + w: along
 // the units either s or w grows from one piece to the next, so no two pieces
 // have one slot.
-constexpr int kStageRows4 = 3;  // 4-bit rows of a page that travel with it; pools with more are read from global memory
 
 struct WalkArgs {
   AttnArgs a;
@@ -51,7 +45,6 @@ struct WalkArgs {
   int64_t* cum;     // [B + 1] own pages before sequence b (written)
 };
 
-__host__ __device__ constexpr int piece_floats(int D, int cols) { return cols * (D + 2); }
 
 // warps that have units (each one at least), the first unit of warp w, and the warp that has unit u
 __device__ __forceinline__ int64_t walkers(int64_t U, int64_t NW) { return U < NW ? U : NW; }
@@ -253,6 +246,7 @@ struct JoinArgs {
   const int64_t* cum;
   int64_t own_nw, front_nw;
   int own_groups, front_groups, own_cols, front_cols;
+  FrontPlan tiles;       // k > 0: the tensor-core kernel's pieces
 };
 
 template <int D, int WPR>
@@ -271,12 +265,12 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinA
   float m = -INFINITY, l = 0.f, o[DL];
 #pragma unroll
   for (int i = 0; i < DL; ++i) o[i] = 0.f;
-  auto add = [&](const float* base, int cols, int col, int64_t first, int64_t n) {
+  auto add = [&](const float* base, int cols, int col, int64_t first, int64_t n, int step = 1) {
     const int64_t size = piece_floats(D, cols);
     for (int64_t i0 = sub; i0 < n; i0 += 32 * WPR) {
       float pm = -INFINITY, pl = 0.f;
       if (i0 + WPR * lane < n) {
-        const float* x = base + (first + i0 + WPR * lane) * size + cols * D + col;
+        const float* x = base + (first + (i0 + WPR * lane) * step) * size + cols * D + col;
         pm = x[0];
         pl = x[cols];
       }
@@ -292,18 +286,19 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinA
 #pragma unroll
       for (int d = 0; d < DL; ++d) o[d] *= f0;
       const int cnt = static_cast<int>(min(static_cast<int64_t>(32), (n - i0 + WPR - 1) / WPR));
-      const float* v = base + (first + i0) * size + col * D + lane * VL;
+      const float* v = base + (first + i0 * step) * size + col * D + lane * VL;
 #pragma unroll 4
       for (int j = 0; j < cnt; ++j) {
         const float fj = __shfl_sync(0xFFFFFFFFu, f, j);
+        if (fj == 0.f) continue;  // nothing seen there, or nothing that counts: its values may be anything
 #pragma unroll
         for (int c = 0; c < DL / VL; ++c) {
           float y[VL];
           if constexpr (VL == 4) {
-            const float4 t = *reinterpret_cast<const float4*>(v + j * WPR * size + 128 * c);
+            const float4 t = *reinterpret_cast<const float4*>(v + j * (WPR * step * size) + 128 * c);
             y[0] = t.x; y[1] = t.y; y[2] = t.z; y[3] = t.w;
           } else {
-            const float2 t = *reinterpret_cast<const float2*>(v + j * WPR * size);
+            const float2 t = *reinterpret_cast<const float2*>(v + j * (WPR * step * size));
             y[0] = t.x; y[1] = t.y;
           }
 #pragma unroll
@@ -322,7 +317,13 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinA
       add(p.own, p.own_cols, r % p.own_cols, static_cast<int64_t>(b) * hg + static_cast<int64_t>(h) * p.own_groups + grp + w0, w1 - w0 + 1);
     }
   }
-  if (p.front != nullptr) {
+  if (p.front != nullptr && p.tiles.k > 0) {
+    const int r = tok * G + gg, tile = r >> 7, k = p.tiles.k;
+    const int64_t item = static_cast<int64_t>(h) * (2 * k * p.tiles.pairs + k * p.tiles.singles);
+    if (front_streams(D) == 1) add(p.front, 128, r & 127, item + tile * k, k);
+    else if (tile < 2 * p.tiles.pairs) add(p.front, 128, r & 127, 2 * (item + (tile >> 1) * 2 * k) + (tile & 1), 2 * k, 2);
+    else add(p.front, 128, r & 127, 2 * (item + p.tiles.pairs * 2 * k), 2 * k);
+  } else if (p.front != nullptr) {
     const int r = tok * G + gg, grp = r / p.front_cols;
     const int64_t seg = static_cast<int64_t>(h) * p.front_groups + grp, U = static_cast<int64_t>(a.n_shared) * a.H * p.front_groups;
     const int64_t nw = walkers(U, p.front_nw), w0 = warp_of(U, seg * a.n_shared, nw), w1 = warp_of(U, (seg + 1) * a.n_shared - 1, nw);
@@ -367,6 +368,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinA
 struct Plan {
   struct Walk { int cols, groups, grid; int64_t nw, slots; };
   Walk own, front;
+  FrontPlan tiles;  // k > 0: the tensor-core kernel has the shared pages
   int64_t off_front, off_cum, bytes;
 };
 
@@ -385,14 +387,38 @@ static Plan::Walk plan_walk(int64_t D, int64_t rows, int64_t segs_per_group, int
   return w;
 }
 
+// Fewest rounds of CTAs x (pages of one + what beginning and ending cost, about 8).
+static FrontPlan plan_tiles(int64_t D, int64_t rows, int64_t H, int64_t n) {
+  const int64_t tiles = (rows + 127) / 128;
+  FrontPlan p{};
+  p.pairs = static_cast<int>(front_streams(static_cast<int>(D)) == 2 ? tiles / 2 : 0);
+  p.singles = static_cast<int>(tiles - 2 * p.pairs);
+  int64_t best = -1;
+  for (int64_t k = 1; k <= n && k <= 64; ++k) {
+    const int64_t items = H * (2 * p.pairs + p.singles) * k;
+    const int64_t cost = (items + num_sms() - 1) / num_sms() * ((n + k - 1) / k + 8);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.k = static_cast<int>(k);
+      p.items = items;
+    }
+  }
+  return p;
+}
+
+constexpr int64_t kTileRows = 5;  // rows from which the tensor-core kernel takes the shared pages
+
 static Plan make_plan(int64_t B, int64_t Sq, int64_t Hq, int64_t H, int64_t D, int64_t n_shared, int64_t W) {
   Plan p{};
   const int64_t rows = Sq * (Hq / H);
   p.own = plan_walk(D, rows, B * H, B * W * H, W > 0);
-  p.front = plan_walk(D, B * rows, H, n_shared * H, n_shared > 0);
+  const bool tiled = n_shared > 0 && B * rows >= kTileRows;
+  if (tiled) p.tiles = plan_tiles(D, B * rows, H, n_shared);
+  p.front = plan_walk(D, B * rows, H, n_shared * H, n_shared > 0 && !tiled);
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   p.off_front = up(p.own.slots * piece_floats(static_cast<int>(D), p.own.cols) * 4);
-  p.off_cum = p.off_front + up(p.front.slots * piece_floats(static_cast<int>(D), p.front.cols) * 4);
+  p.off_cum = p.off_front + up(tiled ? p.tiles.items * front_streams(static_cast<int>(D)) * piece_floats(static_cast<int>(D), 128) * 4
+                                     : p.front.slots * piece_floats(static_cast<int>(D), p.front.cols) * 4);
   p.bytes = p.off_cum + (W > 0 ? up((B + 1) * 8) : 0);
   return p;
 }
@@ -445,6 +471,7 @@ static cudaError_t launch_all(const AttnArgs& a, cudaStream_t s) {
   j.front_groups = pl.front.groups;
   j.own_cols = pl.own.cols;
   j.front_cols = pl.front.cols;
+  j.tiles = pl.tiles;
   int64_t* cum = reinterpret_cast<int64_t*>(a.work + pl.off_cum);
   j.cum = cum;
   bool behind = false;
@@ -460,7 +487,12 @@ static cudaError_t launch_all(const AttnArgs& a, cudaStream_t s) {
   if (a.n_shared > 0) {
     float* parts = reinterpret_cast<float*>(a.work + pl.off_front);
     j.front = parts;
-    e = walk(pl.front, true, parts);
+    if (pl.tiles.k > 0) {
+      e = launch_front(a, pl.tiles, parts, s);
+      behind = true;
+    } else {
+      e = walk(pl.front, true, parts);
+    }
   }
   if (e == cudaSuccess && a.W > 0) {
     float* parts = reinterpret_cast<float*>(a.work);
@@ -472,7 +504,7 @@ static cudaError_t launch_all(const AttnArgs& a, cudaStream_t s) {
   // 7.7 with a block a row); four where one sequence's pages went to many warps.
   const int64_t rows = static_cast<int64_t>(a.B) * a.Sq * a.Hq;
   const int64_t pieces = (j.own ? pl.own.nw / (static_cast<int64_t>(a.B) * a.H * pl.own.groups) + 1 : 0) +
-                         (j.front ? pl.front.nw / (static_cast<int64_t>(a.H) * pl.front.groups) + 1 : 0);
+                         (pl.tiles.k > 0 ? 2 * pl.tiles.k : j.front ? pl.front.nw / (static_cast<int64_t>(a.H) * pl.front.groups) + 1 : 0);
   const bool wide = pieces > 16;
   const dim3 grid(static_cast<unsigned>(wide ? rows : (rows + 3) / 4));
   auto join = wide ? join_kernel<D, 4> : join_kernel<D, 1>;

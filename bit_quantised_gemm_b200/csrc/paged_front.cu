@@ -1,0 +1,533 @@
+// Attention of many query rows over the shared pages of the paged 3-bit cache
+// (layout: paged.cuh), on the 5th-generation tensor cores.
+//
+// The rows of all sequences that read one cache head are the rows of one
+// product: 128 a tile. A CTA takes a range of the shared pages for one head and
+// two "streams": two tiles on the same pages (each page taken apart once for
+// both), or, where a head has an odd tile left, one tile with its even and its
+// odd pages. With D = 256, tensor memory holds one stream.
+//   loader      one warp, bulk copies of a page's block into a ring (V's 16
+//               groups 16 bytes further apart, against bank conflicts)
+//   unpackers   K -> [64 tokens][D], V -> [D][64 tokens] as fp16 codes - 4,
+//               128-byte swizzled; a token kept at 4 bits is one of these rows;
+//               the scales beside them as they are
+//   issuer      S = Q K^T (Q in tensor memory), O += P V (P in tensor memory,
+//               where S was), one thread
+//   softmax     4 warps a stream, a row a thread: s = S x (K scale),
+//               p = 2^(s - r), weights p x (V scale) rounded to fp16 (2^-11 of
+//               a weight, a quarter of what the output's rounding may take).
+//               r is the largest s so far plus the largest V scale's exponent;
+//               it moves, and O is multiplied, only when it grows by 2^8.
+// While one stream's rows are in the softmax, the other's products run.
+//
+// Per tile and page (D = 128) the two products take 512 clocks of the tensor
+// pipe, the 8192 exponentials 512 of the special-function units.
+#include "launch.h"
+#include "paged.cuh"
+#include "paged_mma.cuh"
+#include "paged_front.cuh"
+#include "ptx.cuh"
+
+namespace blt {
+namespace paged {
+namespace {
+
+template <int D>
+struct Shape {
+  static constexpr int STREAMS = front_streams(D);
+  static constexpr int SBUF = D == 128 ? 1 : 2;      // S buffers of a stream
+  static constexpr int NST = D == 256 ? 2 : 4;       // K and V tiles
+  static constexpr int NRAW = D == 256 ? 3 : 4;      // blocks as they come
+  static constexpr int SOFT = 4 * STREAMS, UNPACK = D == 256 ? 8 : 4;  // warps
+  static constexpr int LOADER = SOFT + UNPACK, ISSUER = LOADER + 1, THREADS = 32 * (ISSUER + 1);
+  static constexpr int RB = row_bytes(D), GS = 4 * RB + 16;  // GS: stride of V's groups of 4 tokens
+  static constexpr int RAW_V = PT * RB, RAW_S = RAW_V + 16 * GS, RAW_4 = RAW_S + 8 * PT;
+  static constexpr int TILE = PT * D * 2;
+  static constexpr int O = 0, Q = STREAMS * D, S = Q + STREAMS * (D / 2);  // tensor memory columns
+  static_assert(S + STREAMS * SBUF * PT <= 512);
+};
+
+template <int D>
+struct Shared {
+  using H = Shape<D>;
+  float ks[H::NST][PT], vs[H::NST][PT];
+  uint64_t dead[H::NST];  // tokens that take no part
+  int v_exp[H::NST];      // biased exponent of the largest V scale
+  int page[H::NRAW];
+  uint64_t raw_full[H::NRAW], raw_empty[H::NRAW], k_full[H::NST], k_empty[H::NST], v_full[H::NST], v_empty[H::NST], sc_full[H::NST];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], drain;
+  uint32_t tmem;
+  int abort;
+  int seen[H::UNPACK];
+};
+
+// D[tmem] (+)= A[tmem] B[smem]^T, fp16 x fp16 -> fp32
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+
+// a code of a 4-bit row as fp16 (c - 8) 2^(j - 9): exact
+__device__ __forceinline__ uint32_t four_bits(uint32_t c, int j) {
+  const __half h = __float2half_rn(static_cast<float>(static_cast<int>(c & 15u) - 8) * (static_cast<float>(1 << j) / 512.f));
+  return __half_as_ushort(h);
+}
+
+template <int D>
+__global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __grid_constant__ FrontArgs p) {
+  using H = Shape<D>;
+  constexpr int STREAMS = H::STREAMS, SBUF = H::SBUF, NST = H::NST, NRAW = H::NRAW, RB = H::RB, GS = H::GS;
+  extern __shared__ __align__(1024) uint8_t dyn[];
+  __shared__ Shared<D> sm;
+  const AttnArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  uint8_t* base = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+  uint8_t* k_tile = base;
+  uint8_t* v_tile = base + NST * H::TILE;
+  uint8_t* raw = base + 2 * NST * H::TILE;
+
+  // ---- the item: head, tiles, pages
+  const int per_head = p.plan.pairs * 2 * p.plan.k + p.plan.singles * p.plan.k;
+  const int item = blockIdx.x, h = item / per_head;
+  int split = item - h * per_head, parts = 2 * p.plan.k, tile0 = 0;
+  const bool pair = split < p.plan.pairs * 2 * p.plan.k;
+  if (pair) {
+    tile0 = 2 * (split / parts);
+    split %= parts;
+  } else {
+    split -= p.plan.pairs * 2 * p.plan.k;
+    parts = p.plan.k;
+    tile0 = 2 * p.plan.pairs + split / parts;
+    split %= parts;
+  }
+  const int first = static_cast<int>(static_cast<int64_t>(a.n_shared) * split / parts);
+  const int n = static_cast<int>(static_cast<int64_t>(a.n_shared) * (split + 1) / parts) - first;
+  const int G = a.Hq / a.H, rows = a.B * a.Sq * G;
+  const bool alternate = STREAMS == 2 && !pair;
+  auto stream_pages = [&](int t) { return alternate ? (n - t + 1) >> 1 : n; };
+  auto stream_rows = [&](int t) { return min(128, rows - 128 * (tile0 + (pair ? t : 0))); };
+
+  if (tid == 0) {
+    for (int i = 0; i < NRAW; ++i) { mbar_init(&sm.raw_full[i], 1); mbar_init(&sm.raw_empty[i], H::UNPACK); }
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&sm.k_full[i], H::UNPACK); mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.v_full[i], H::UNPACK); mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.sc_full[i], 1);
+    }
+    for (int t = 0; t < STREAMS; ++t) {
+      const int live = (stream_rows(t) + 31) / 32;
+      mbar_init(&sm.q_full[t], live);
+      for (int b = 0; b < SBUF; ++b) { mbar_init(&sm.s_full[t][b], 1); mbar_init(&sm.p_full[t][b], live); }
+      mbar_init(&sm.pv_done[t], 1);
+    }
+    mbar_init(&sm.drain, 1);
+    sm.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == H::ISSUER) { tmem_alloc(&sm.tmem, 512); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  pdl_wait();
+  pdl_trigger();
+  const uint32_t tm = sm.tmem;
+  volatile int* abort = &sm.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(bar, parity & 1u, a.timeout_ns, abort)) return true;
+    *abort = 1;
+    return false;
+  };
+
+  if (warp == H::LOADER) {
+    const int c4_bytes = p.c4_bytes;
+    int ids = 0, put = 0;
+    bool ok = true;
+    for (; put < n; ++put) {
+      if ((put & 31) == 0) ids = put + lane < n ? __ldg(a.shared + first + put + lane) : 0;
+      const int page = __shfl_sync(0xFFFFFFFFu, ids, put & 31);
+      const int st = put % NRAW;
+      if (put >= NRAW) ok = wait(&sm.raw_empty[st], put / NRAW - 1);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      const bool good = page >= 0 && page < a.n_pages;
+      if (lane == 0) {
+        sm.page[st] = good ? page : -1;
+        if (good) mbar_arrive_expect_tx(&sm.raw_full[st], static_cast<uint32_t>(block_bytes(D) + c4_bytes));
+        else { report_status(a.status, BITLINEAR_STATUS_BAD_INDEX); mbar_arrive(&sm.raw_full[st]); }
+      }
+      __syncwarp();
+      if (good) {
+        const int64_t at = static_cast<int64_t>(page) * a.H + h;
+        const uint8_t* blk = a.pages + at * block_bytes(D);
+        uint8_t* dst = raw + st * p.raw_bytes;
+        if (lane < 16) bulk_load(dst + H::RAW_V + lane * GS, blk + off_v(D) + lane * 4 * RB, 4 * RB, &sm.raw_full[st]);
+        else if (lane == 16) bulk_load(dst, blk, PT * RB, &sm.raw_full[st]);
+        else if (lane == 17) bulk_load(dst + H::RAW_S, blk + off_ks(D), 8 * PT, &sm.raw_full[st]);
+        else if (lane == 18 && c4_bytes) bulk_load(dst + H::RAW_4, a.codes4 + at * c4_bytes, c4_bytes, &sm.raw_full[st]);
+      }
+    }
+    if (*abort)  // copies in flight land before the memory is released
+      for (int i = max(0, put - NRAW); i < put; ++i) mbar_wait(&sm.raw_full[i % NRAW], (i / NRAW) & 1, a.timeout_ns, nullptr);
+  } else if (warp == H::ISSUER) {
+    if (elect_one()) {
+      constexpr uint32_t idS = make_idesc(1, 0, 0, 128, PT), idO = make_idesc(1, 0, 0, 128, D);
+      int n_s[2] = {0, 0};
+      bool ok = true;
+      auto issue_s = [&](int t) {
+        const int k = n_s[t]++, pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
+        if (!(ok = wait(&sm.k_full[st], pg / NST))) return;
+        tc_fence_after();
+        const uint32_t kt = smem_u32(k_tile + st * H::TILE);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          mma_f16_ts(tm + H::S + (t * SBUF + b) * PT, tm + H::Q + t * (D / 2) + 8 * i, smem_desc_sw128(kt + (i >> 2) * (PT * 128) + (i & 3) * 32), idS, i > 0);
+        tc_commit(&sm.s_full[t][b]);
+        if (alternate || t == STREAMS - 1) tc_commit(&sm.k_empty[st]);
+      };
+      for (int t = 0; t < STREAMS && ok; ++t)
+        if (stream_pages(t) > 0) ok = wait(&sm.q_full[t], 0);
+      tc_fence_after();
+      for (int b = 0; b < SBUF; ++b)
+        for (int t = 0; t < STREAMS; ++t)
+          if (ok && b < stream_pages(t)) issue_s(t);
+      for (int k = 0; k < stream_pages(0) && ok; ++k)
+        for (int t = 0; t < STREAMS; ++t) {
+          if (!ok || k >= stream_pages(t)) continue;
+          const int pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
+          if (!(ok = wait(&sm.v_full[st], pg / NST) && wait(&sm.p_full[t][b], k / SBUF))) break;
+          tc_fence_after();
+          const uint32_t vt = smem_u32(v_tile + st * H::TILE);
+#pragma unroll
+          for (int i = 0; i < PT / 16; ++i)
+            mma_f16_ts(tm + H::O + t * D, tm + H::S + (t * SBUF + b) * PT + 8 * i, smem_desc_sw128(vt + i * 32), idO, k > 0 || i > 0);
+          tc_commit(&sm.pv_done[t]);
+          if (alternate || t == STREAMS - 1) tc_commit(&sm.v_empty[st]);
+          if (n_s[t] < stream_pages(t)) issue_s(t);
+        }
+      if (!ok) {  // what was issued ends before the memory is released
+        tc_commit(&sm.drain);
+        mbar_wait(&sm.drain, 0, a.timeout_ns, nullptr);
+      }
+    }
+    __syncwarp();
+  } else if (warp >= H::SOFT) {
+    // ------------------------------------------------------------ unpackers
+    const int ut = tid - 32 * H::SOFT, uw = warp - H::SOFT;
+    int seen = 0;  // tokens that any row sees
+    for (int b = ut; b < a.B; b += 32 * H::UNPACK) {
+      bool bad;
+      seen = max(seen, cut_len(a, b, &bad));
+      if (bad && item == 0) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
+    }
+    seen = __reduce_max_sync(0xFFFFFFFFu, seen);
+    if (lane == 0) sm.seen[uw] = seen;
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * H::UNPACK) : "memory");
+#pragma unroll
+    for (int i = 0; i < H::UNPACK; ++i) seen = max(seen, sm.seen[i]);
+    for (int pg = 0; pg < n; ++pg) {
+      const int rs = pg % NRAW, st = pg % NST;
+      bool ok = true;
+      if (pg >= NST) ok = wait(&sm.v_empty[st], pg / NST - 1) && wait(&sm.k_empty[st], pg / NST - 1);
+      ok = ok && wait(&sm.raw_full[rs], pg / NRAW);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      const uint8_t* src = raw + rs * p.raw_bytes;
+      const float* scales = reinterpret_cast<const float*>(src + H::RAW_S);
+      const int page = sm.page[rs];
+      const int live = page < 0 ? 0 : min(PT, seen - (first + pg) * PT);  // tokens of the page that any row sees
+      auto row4 = [&](int j) {
+        return p.c4_bytes ? src + H::RAW_4 + j * D : a.codes4 + ((static_cast<int64_t>(page) * a.H + h) * a.C4 + j) * D;
+      };
+      if (uw == 0) {  // scales
+        uint32_t dead[2];
+        int top = 14;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int o = lane + 32 * i;
+          const float ks = scales[o], vs = scales[PT + o];
+          const bool use = o < live;
+          const bool bad4 = use && signbit(ks) && src[o * RB] >= a.C4;
+          if (bad4) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
+          dead[i] = __ballot_sync(0xFFFFFFFFu, !use || bad4);
+          sm.ks[st][o] = use ? fabsf(ks) : 0.f;
+          sm.vs[st][o] = use ? vs : 0.f;
+          if (use) top = max(top, __float_as_int(vs) >> 23);
+        }
+        top = __reduce_max_sync(0xFFFFFFFFu, top);
+        if (lane == 0) {
+          sm.v_exp[st] = top;
+          sm.dead[st] = static_cast<uint64_t>(dead[1]) << 32 | dead[0];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.sc_full[st]);
+      }
+      // K: a lane a token's chunk of 32 codes; 8 (16) tokens x 4 (2) chunks a warp: no bank conflicts
+      constexpr int CH = D / 32, CW = CH < 4 ? CH : 4, TW = 32 / CW;
+#pragma unroll
+      for (int it = 0; it < PT * CH / (32 * H::UNPACK); ++it) {
+        const int step = it * H::UNPACK + uw;
+        const int o = step / (CH / CW) * TW + lane % TW, c = step % (CH / CW) * CW + lane / TW;
+        uint32_t x[16];
+        if (page >= 0) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(src + o * RB + 12 * c);
+          const uint32_t X[3] = {w[0], w[1], w[2]};
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = k_operand(X, pair32(i));
+          if (a.C4 > 0 && o < live && signbit(scales[o]) && src[o * RB] < a.C4) {
+            const uint32_t* r4 = reinterpret_cast<const uint32_t*>(row4(src[o * RB]) + 16 * c);
+            const uint32_t y[4] = {r4[0], r4[1], r4[2], r4[3]};
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const Pair pr = pair32(i);
+              x[i] = four_bits(y[pr.lo >> 3] >> (4 * (pr.lo & 7)), 3 * pr.lo - pr.n) |
+                     four_bits(y[pr.hi >> 3] >> (4 * (pr.hi & 7)), 3 * pr.hi - pr.n - 16) << 16;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[i] = 0u;
+        }
+        const uint32_t dst = smem_u32(k_tile + st * H::TILE) + (c >> 1) * (PT * 128) + o * 128;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) st_shared_v4(dst + ((((c & 1) * 4 + i) ^ (o & 7)) << 4), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.k_full[st]);
+      // V: a lane 8 dimensions of 8 tokens
+      if (ut < D) {
+        const int e = lane & 7, dg = ut >> 3;
+        uint32_t x[8][4];
+        if (page >= 0) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const uint32_t* w = reinterpret_cast<const uint32_t*>(src + H::RAW_V + (2 * e + q) * GS + 12 * dg);
+            const uint32_t X[3] = {w[0], w[1], w[2]}, Y[3] = {X[0] >> 8, X[1] >> 8, X[2] >> 8};
+            v_operand<0>(X, Y, x[0][2 * q], x[0][2 * q + 1]);
+            v_operand<1>(X, Y, x[1][2 * q], x[1][2 * q + 1]);
+            v_operand<2>(X, Y, x[2][2 * q], x[2][2 * q + 1]);
+            v_operand<3>(X, Y, x[3][2 * q], x[3][2 * q + 1]);
+            v_operand<4>(X, Y, x[4][2 * q], x[4][2 * q + 1]);
+            v_operand<5>(X, Y, x[5][2 * q], x[5][2 * q + 1]);
+            v_operand<6>(X, Y, x[6][2 * q], x[6][2 * q + 1]);
+            v_operand<7>(X, Y, x[7][2 * q], x[7][2 * q + 1]);
+          }
+          if (a.C4 > 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int o = 8 * e + i;
+              if (o < live && signbit(scales[o]) && src[o * RB] < a.C4) {
+                const uint32_t y = *reinterpret_cast<const uint32_t*>(row4(src[o * RB]) + D / 2 + 4 * dg);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) {  // token i: word 2 (i / 4) + i % 2, half i / 2 % 2
+                  uint32_t& z = x[d][2 * (i >> 2) + (i & 1)];
+                  const uint32_t v = four_bits(y >> (4 * d), v_bit(d));
+                  z = (i & 2) ? (z & 0xFFFFu) | v << 16 : (z & 0xFFFF0000u) | v;
+                }
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[d][i] = 0u;
+        }
+        const uint32_t dst = smem_u32(v_tile + st * H::TILE) + dg * 1024;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) st_shared_v4(dst + d * 128 + ((e ^ d) << 4), x[d][0], x[d][1], x[d][2], x[d][3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) { mbar_arrive(&sm.v_full[st]); mbar_arrive(&sm.raw_empty[rs]); }
+    }
+  } else {
+    // -------------------------------------------------------------- softmax
+    const int t = warp >> 2, np = stream_pages(t);
+    const int r0 = 128 * (tile0 + (pair ? t : 0)) + 32 * (warp & 3), r = r0 + lane;
+    float* out = p.parts + (static_cast<int64_t>(item) * STREAMS + t) * piece_floats(D, 128);
+    const int col = 32 * (warp & 3) + lane;
+    if (r0 < rows) {
+      const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+      const Segment sg{0, 0, rows, h, G, true};
+      const int sees = row_sees(a, sg, r) - first * PT;  // from the item's first page on
+      float kq = 0.f;
+      if (np > 0) {  // the row's query: fp16, its largest value in [2^14, 2^15)
+        const uint16_t* q = r < rows ? query_row(a, sg, r) : nullptr;
+        uint32_t am = 0u;
+        if (q != nullptr)
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + i);
+            am = max(am, max(max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)),
+                             max(max(v.z & 0x7FFFu, (v.z >> 16) & 0x7FFFu), max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu))));
+          }
+        const int fb = min(268 - max(1, static_cast<int>(am >> 7)), 254);
+        const float f = pow2_biased(fb);
+        kq = a.qk_scale * 1.4426950408889634f * pow2_biased(263 - fb);
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t x[32], y[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q) + 8 * c + i) : make_uint4(0u, 0u, 0u, 0u);
+            x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+          }
+          auto qf = [&](int d) { return __uint_as_float((d & 1) ? (x[d >> 1] & 0xFFFF0000u) : (x[d >> 1] << 16)) * f; };
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const Pair pr = pair32(i & 15);
+            const int d0 = 32 * (i >> 4);
+            y[i] = pack_f16x2(qf(d0 + pr.lo) * (1.f / (1 << (3 * pr.lo - pr.n))), qf(d0 + pr.hi) * (1.f / (1 << (3 * pr.hi - pr.n - 16))));
+          }
+          tmem_st32(tm + lanes + H::Q + t * (D / 2) + 32 * c, y);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_full[t]);
+      }
+      const int n_all = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<unsigned>(max(sees, 0))) / PT);
+      float ref = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int k = 0; k < np; ++k) {
+        const int pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
+        const uint32_t s_col = tm + lanes + H::S + (t * SBUF + b) * PT;
+        ok = wait(&sm.s_full[t][b], k / SBUF) && wait(&sm.sc_full[st], pg / NST);
+        if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+        tc_fence_after();
+        float s[PT];
+        {
+          uint32_t x[PT];
+          tmem_ld64(s_col, x);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < PT; i += 4) {
+            const float4 ks = *reinterpret_cast<const float4*>(&sm.ks[st][i]);
+            const float2 u = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(ks.x, ks.y));
+            const float2 v = mul2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(ks.z, ks.w));
+            s[i] = u.x; s[i + 1] = u.y; s[i + 2] = v.x; s[i + 3] = v.y;
+          }
+        }
+        const uint64_t dead = sm.dead[st];
+        if (pg >= n_all || dead != 0) {
+          const int lim = sees - pg * PT;
+#pragma unroll
+          for (int i = 0; i < PT; ++i)
+            if (i >= lim || ((dead >> i) & 1)) s[i] = -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < PT; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+        // weights stay below 2^15: p <= 2^8, V scales x 2^(133 - v_exp) below 2^7
+        const float want = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kq + static_cast<float>(sm.v_exp[st] - 133);
+        const bool grow = want > ref + 8.f || (ref == -INFINITY && want > -INFINITY);
+        if (__any_sync(0xFFFFFFFFu, grow)) {
+          const float now = grow ? want : ref;
+          const float f = ref == -INFINITY ? 0.f : ex2(ref - now);
+          if (k > 0) {
+            ok = wait(&sm.pv_done[t], k - 1);
+            if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t x[32];
+              tmem_ld32(tm + lanes + H::O + t * D + 32 * c, x);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+              tmem_st32(tm + lanes + H::O + t * D + 32 * c, x);
+            }
+            tmem_st_wait();
+          }
+          l *= f;
+          ref = now;
+        }
+        const float mr = ref == -INFINITY ? 0.f : ref;
+        float sum[2] = {0.f, 0.f};
+        // the words of P: V's order within 4 tokens is 0, 2, 1, 3
+        uint32_t w[PT / 2];
+#pragma unroll
+        for (int i = 0; i < PT; i += 4) {
+          const float4 vs = *reinterpret_cast<const float4*>(&sm.vs[st][i]);
+          float e[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            e[c] = ex2(fmaf(s[i + c], kq, -mr));
+            sum[c & 1] += e[c];
+          }
+          const float2 u = mul2(make_float2(e[0], e[2]), make_float2(vs.x, vs.z));
+          const float2 v = mul2(make_float2(e[1], e[3]), make_float2(vs.y, vs.w));
+          w[i / 2] = pack_f16x2(u.x, u.y);
+          w[i / 2 + 1] = pack_f16x2(v.x, v.y);
+        }
+        l += sum[0] + sum[1];
+        tmem_st32(s_col, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.p_full[t][b]);
+      }
+      // ---- the piece
+      if (ok && np > 0) {
+        ok = wait(&sm.pv_done[t], np - 1);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        tc_fence_after();
+      }
+      if (ok) {
+        if (np > 0)
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            tmem_ld32(tm + lanes + H::O + t * D + 32 * c, x);
+            tmem_ld_wait();
+            if (r < rows) {
+              float4* dst = reinterpret_cast<float4*>(out + col * D + 32 * c);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                dst[i] = make_float4(__uint_as_float(x[4 * i]) * (512.f / (1 << v_bit((4 * i) & 7))), __uint_as_float(x[4 * i + 1]) * (512.f / (1 << v_bit((4 * i + 1) & 7))),
+                                     __uint_as_float(x[4 * i + 2]) * (512.f / (1 << v_bit((4 * i + 2) & 7))), __uint_as_float(x[4 * i + 3]) * (512.f / (1 << v_bit((4 * i + 3) & 7))));
+            }
+          }
+        if (r < rows) {
+          out[128 * D + col] = ref;
+          out[128 * D + 128 + col] = l;
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (tid == 0 && sm.abort) report_status(a.status, BITLINEAR_STATUS_TIMEOUT);
+  if (warp == H::ISSUER) tmem_dealloc(tm, 512);
+}
+
+template <int D>
+cudaError_t launch_front_t(const AttnArgs& a, const FrontPlan& plan, float* parts, cudaStream_t s) {
+  using H = Shape<D>;
+  FrontArgs p{};
+  p.a = a;
+  p.plan = plan;
+  p.parts = parts;
+  p.c4_bytes = a.C4 <= kStageRows4 ? a.C4 * D : 0;
+  p.raw_bytes = H::RAW_4 + p.c4_bytes;
+  const int smem = 1024 + 2 * H::NST * H::TILE + H::NRAW * p.raw_bytes;
+  const cudaError_t e = set_smem_limit(front_kernel<D>, smem);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(front_kernel<D>, dim3(static_cast<unsigned>(plan.items)), dim3(H::THREADS), smem, s, 0u, p);
+}
+
+}  // namespace
+
+cudaError_t launch_front(const AttnArgs& a, const FrontPlan& plan, float* parts, cudaStream_t s) {
+  if (a.D == 64) return launch_front_t<64>(a, plan, parts, s);
+  if (a.D == 128) return launch_front_t<128>(a, plan, parts, s);
+  return launch_front_t<256>(a, plan, parts, s);
+}
+
+}  // namespace paged
+}  // namespace blt

@@ -9,6 +9,17 @@
 namespace blt {
 namespace paged {
 
+constexpr int kStageRows4 = 3;  // 4-bit rows of a page that travel with it; pools with more are read from global memory
+
+// A piece: [cols][D] value sums, then [cols] maxima, then [cols] sums.
+__host__ __device__ constexpr int piece_floats(int D, int cols) { return cols * (D + 2); }
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
 __device__ __forceinline__ int cut_len(const AttnArgs& a, int b, bool* bad) {
   const int64_t cap = static_cast<int64_t>(a.n_shared + a.W) * PT;
   const int len = __ldg(a.lens + b);
