@@ -9,19 +9,20 @@
 //   loader      one warp, bulk copies of a page's block into a ring (V's 16
 //               groups 16 bytes further apart, against bank conflicts)
 //   unpackers   K -> [64 tokens][D], V -> [D][64 tokens] as fp16 codes - 4,
-//               128-byte swizzled; a token kept at 4 bits is one of these rows;
-//               the scales beside them as they are
-//   issuer      S = Q K^T (Q in tensor memory), O += P V (P in tensor memory,
-//               where S was), one thread
-//   softmax     4 warps a stream, a row a thread: s = S x (K scale),
-//               p = 2^(s - r), weights p x (V scale) rounded to fp16 (2^-11 of
-//               a weight, a quarter of what the output's rounding may take).
-//               r is the largest s so far plus the largest V scale's exponent;
-//               it moves, and O is multiplied, only when it grows by 2^8.
+//               128-byte swizzled; a token kept at 4 bits is one of these rows
+//   scaler      one warp, the scales beside them, and which tokens take part
+//   issuer      one thread: S = Q K^T, O += P V (P in tensor memory where S
+//               was; two S a stream, so that the next one is there when a
+//               softmax ends)
+//   softmax     8 warps a stream, half a row's tokens a thread: s = S x (K
+//               scale), p = 2^(s - r), weights p x (V scale) rounded to fp16
+//               (2^-11 of a weight, a quarter of what the output's rounding
+//               may take). r is the largest s so far plus the largest V scale's
+//               exponent; it moves, and O is multiplied, only when it grows by 8.
 // While one stream's rows are in the softmax, the other's products run.
 //
-// Per tile and page (D = 128) the two products take 512 clocks of the tensor
-// pipe, the 8192 exponentials 512 of the special-function units.
+// Q is in tensor memory where there is room for it beside two S a stream (D =
+// 64 and 256), in shared memory else.
 #include "launch.h"
 #include "paged.cuh"
 #include "paged_mma.cuh"
@@ -35,15 +36,16 @@ namespace {
 template <int D>
 struct Shape {
   static constexpr int STREAMS = front_streams(D);
-  static constexpr int SBUF = D == 128 ? 1 : 2;      // S buffers of a stream
+  static constexpr int SBUF = 2;                     // S buffers of a stream
+  static constexpr bool QS = D == 128;               // Q in shared memory
   static constexpr int NST = D == 256 ? 2 : 4;       // K and V tiles
-  static constexpr int NRAW = D == 256 ? 3 : 4;      // blocks as they come
-  static constexpr int SOFT = 4 * STREAMS, UNPACK = D == 256 ? 8 : 4;  // warps
-  static constexpr int LOADER = SOFT + UNPACK, ISSUER = LOADER + 1, THREADS = 32 * (ISSUER + 1);
+  static constexpr int NRAW = 3;                     // blocks as they come
+  static constexpr int SOFT = 8 * STREAMS, UNPACK = D == 256 ? 8 : 4;  // warps
+  static constexpr int LOADER = SOFT + UNPACK, SCALER = LOADER + 1, ISSUER = SCALER + 1, THREADS = 32 * (ISSUER + 1);
   static constexpr int RB = row_bytes(D), GS = 4 * RB + 16;  // GS: stride of V's groups of 4 tokens
   static constexpr int RAW_V = PT * RB, RAW_S = RAW_V + 16 * GS, RAW_4 = RAW_S + 8 * PT;
-  static constexpr int TILE = PT * D * 2;
-  static constexpr int O = 0, Q = STREAMS * D, S = Q + STREAMS * (D / 2);  // tensor memory columns
+  static constexpr int TILE = PT * D * 2, Q_TILE = QS ? 128 * D * 2 : 0;
+  static constexpr int O = 0, Q = STREAMS * D, S = Q + (QS ? 0 : STREAMS * (D / 2));  // tensor memory columns
   static_assert(S + STREAMS * SBUF * PT <= 512);
 };
 
@@ -54,11 +56,11 @@ struct Shared {
   uint64_t dead[H::NST];  // tokens that take no part
   int v_exp[H::NST];      // biased exponent of the largest V scale
   int page[H::NRAW];
-  uint64_t raw_full[H::NRAW], raw_empty[H::NRAW], k_full[H::NST], k_empty[H::NST], v_full[H::NST], v_empty[H::NST], sc_full[H::NST];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], drain;
+  uint64_t raw_full[H::NRAW], raw_empty[H::NRAW], k_full[H::NST], v_full[H::NST], v_empty[H::NST], sc_full[H::NST];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], meet[2][4], drain;
   uint32_t tmem;
   int abort;
-  int seen[H::UNPACK];
+  float top[2][2][2][128];  // [stream][page's parity][half]: a row's largest score of a half
 };
 
 // D[tmem] (+)= A[tmem] B[smem]^T, fp16 x fp16 -> fp32
@@ -71,13 +73,38 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       : "memory");
 }
 
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
 
-// a code of a 4-bit row as fp16 (c - 8) 2^(j - 9): exact
-__device__ __forceinline__ uint32_t four_bits(uint32_t c, int j) {
-  const __half h = __float2half_rn(static_cast<float>(static_cast<int>(c & 15u) - 8) * (static_cast<float>(1 << j) / 512.f));
-  return __half_as_ushort(h);
+// two codes of a 4-bit row (in the low nibbles of the halves) as fp16 (c - 8) 2^(j - 9): exact
+__device__ __forceinline__ uint32_t four_bits(uint32_t x, int jl, int jh) {
+  const uint32_t scale = (jl + 6) << 10 | (jh + 6) << 26;  // 2^(j - 9)
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"((x & 0x000F000Fu) | 0x64006400u), "r"(0x64086408u));  // 1024 + c - 1032
+  asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(r) : "r"(scale));
+  return r;
 }
+
+__constant__ uint8_t kPairs[16][4] = {  // pair32's codes and their bits in the halves
+#define BLT_P(I) {pair32(I).lo, pair32(I).hi, 3 * pair32(I).lo - pair32(I).n, 3 * pair32(I).hi - pair32(I).n - 16}
+    BLT_P(0), BLT_P(1), BLT_P(2), BLT_P(3), BLT_P(4), BLT_P(5), BLT_P(6), BLT_P(7),
+    BLT_P(8), BLT_P(9), BLT_P(10), BLT_P(11), BLT_P(12), BLT_P(13), BLT_P(14), BLT_P(15)};
+#undef BLT_P
 
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __grid_constant__ FrontArgs p) {
@@ -88,9 +115,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   uint8_t* base = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
-  uint8_t* k_tile = base;
-  uint8_t* v_tile = base + NST * H::TILE;
-  uint8_t* raw = base + 2 * NST * H::TILE;
+  uint8_t* q_tile = base;
+  uint8_t* k_tile = base + STREAMS * H::Q_TILE;
+  uint8_t* v_tile = k_tile + NST * H::TILE;
+  uint8_t* raw = v_tile + NST * H::TILE;
 
   // ---- the item: head, tiles, pages
   const int per_head = p.plan.pairs * 2 * p.plan.k + p.plan.singles * p.plan.k;
@@ -114,17 +142,18 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
   auto stream_rows = [&](int t) { return min(128, rows - 128 * (tile0 + (pair ? t : 0))); };
 
   if (tid == 0) {
-    for (int i = 0; i < NRAW; ++i) { mbar_init(&sm.raw_full[i], 1); mbar_init(&sm.raw_empty[i], H::UNPACK); }
+    for (int i = 0; i < NRAW; ++i) { mbar_init(&sm.raw_full[i], 1); mbar_init(&sm.raw_empty[i], H::UNPACK + 1); }
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&sm.k_full[i], H::UNPACK); mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.k_full[i], H::UNPACK);
       mbar_init(&sm.v_full[i], H::UNPACK); mbar_init(&sm.v_empty[i], 1);
       mbar_init(&sm.sc_full[i], 1);
     }
     for (int t = 0; t < STREAMS; ++t) {
-      const int live = (stream_rows(t) + 31) / 32;
+      const int live = 2 * ((stream_rows(t) + 31) / 32);  // warps with rows
       mbar_init(&sm.q_full[t], live);
       for (int b = 0; b < SBUF; ++b) { mbar_init(&sm.s_full[t][b], 1); mbar_init(&sm.p_full[t][b], live); }
       mbar_init(&sm.pv_done[t], 1);
+      for (int i = 0; i < 4; ++i) mbar_init(&sm.meet[t][i], 2);
     }
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -180,14 +209,16 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       bool ok = true;
       auto issue_s = [&](int t) {
         const int k = n_s[t]++, pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
-        if (!(ok = wait(&sm.k_full[st], pg / NST))) return;
+        if ((alternate || t == 0) && !(ok = wait(&sm.k_full[st], pg / NST))) return;
         tc_fence_after();
-        const uint32_t kt = smem_u32(k_tile + st * H::TILE);
+        const uint32_t kt = smem_u32(k_tile + st * H::TILE), d = tm + H::S + (t * SBUF + b) * PT;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
-          mma_f16_ts(tm + H::S + (t * SBUF + b) * PT, tm + H::Q + t * (D / 2) + 8 * i, smem_desc_sw128(kt + (i >> 2) * (PT * 128) + (i & 3) * 32), idS, i > 0);
+        for (int i = 0; i < D / 16; ++i) {
+          const uint64_t bd = smem_desc_sw128(kt + (i >> 2) * (PT * 128) + (i & 3) * 32);
+          if constexpr (H::QS) mma_f16_ss(d, smem_desc_sw128(smem_u32(q_tile + t * H::Q_TILE) + (i >> 2) * (128 * 128) + (i & 3) * 32), bd, idS, i > 0);
+          else mma_f16_ts(d, tm + H::Q + t * (D / 2) + 8 * i, bd, idS, i > 0);
+        }
         tc_commit(&sm.s_full[t][b]);
-        if (alternate || t == STREAMS - 1) tc_commit(&sm.k_empty[st]);
       };
       for (int t = 0; t < STREAMS && ok; ++t)
         if (stream_pages(t) > 0) ok = wait(&sm.q_full[t], 0);
@@ -199,7 +230,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         for (int t = 0; t < STREAMS; ++t) {
           if (!ok || k >= stream_pages(t)) continue;
           const int pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
-          if (!(ok = wait(&sm.v_full[st], pg / NST) && wait(&sm.p_full[t][b], k / SBUF))) break;
+          if (alternate || t == 0) ok = wait(&sm.v_full[st], pg / NST);
+          if (!(ok = ok && wait(&sm.p_full[t][b], k / SBUF))) break;
           tc_fence_after();
           const uint32_t vt = smem_u32(v_tile + st * H::TILE);
 #pragma unroll
@@ -215,131 +247,136 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       }
     }
     __syncwarp();
-  } else if (warp >= H::SOFT) {
-    // ------------------------------------------------------------ unpackers
-    const int ut = tid - 32 * H::SOFT, uw = warp - H::SOFT;
+  } else if (warp == H::SCALER) {
     int seen = 0;  // tokens that any row sees
-    for (int b = ut; b < a.B; b += 32 * H::UNPACK) {
+    for (int b = lane; b < a.B; b += 32) {
       bool bad;
       seen = max(seen, cut_len(a, b, &bad));
       if (bad && item == 0) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
     }
     seen = __reduce_max_sync(0xFFFFFFFFu, seen);
-    if (lane == 0) sm.seen[uw] = seen;
-    asm volatile("bar.sync 1, %0;" ::"n"(32 * H::UNPACK) : "memory");
-#pragma unroll
-    for (int i = 0; i < H::UNPACK; ++i) seen = max(seen, sm.seen[i]);
     for (int pg = 0; pg < n; ++pg) {
       const int rs = pg % NRAW, st = pg % NST;
-      bool ok = true;
-      if (pg >= NST) ok = wait(&sm.v_empty[st], pg / NST - 1) && wait(&sm.k_empty[st], pg / NST - 1);
+      bool ok = pg < NST || wait(&sm.v_empty[st], pg / NST - 1);
       ok = ok && wait(&sm.raw_full[rs], pg / NRAW);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       const uint8_t* src = raw + rs * p.raw_bytes;
       const float* scales = reinterpret_cast<const float*>(src + H::RAW_S);
-      const int page = sm.page[rs];
-      const int live = page < 0 ? 0 : min(PT, seen - (first + pg) * PT);  // tokens of the page that any row sees
-      auto row4 = [&](int j) {
-        return p.c4_bytes ? src + H::RAW_4 + j * D : a.codes4 + ((static_cast<int64_t>(page) * a.H + h) * a.C4 + j) * D;
-      };
-      if (uw == 0) {  // scales
-        uint32_t dead[2];
-        int top = 14;
+      const int live = sm.page[rs] < 0 ? 0 : min(PT, seen - (first + pg) * PT);
+      uint32_t dead[2];
+      int top = 14;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int o = lane + 32 * i;
-          const float ks = scales[o], vs = scales[PT + o];
-          const bool use = o < live;
-          const bool bad4 = use && signbit(ks) && src[o * RB] >= a.C4;
-          if (bad4) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
-          dead[i] = __ballot_sync(0xFFFFFFFFu, !use || bad4);
-          sm.ks[st][o] = use ? fabsf(ks) : 0.f;
-          sm.vs[st][o] = use ? vs : 0.f;
-          if (use) top = max(top, __float_as_int(vs) >> 23);
-        }
-        top = __reduce_max_sync(0xFFFFFFFFu, top);
-        if (lane == 0) {
-          sm.v_exp[st] = top;
-          sm.dead[st] = static_cast<uint64_t>(dead[1]) << 32 | dead[0];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.sc_full[st]);
+      for (int i = 0; i < 2; ++i) {
+        const int o = lane + 32 * i;
+        const float ks = scales[o], vs = scales[PT + o];
+        const bool use = o < live;
+        const bool bad4 = use && signbit(ks) && src[o * RB] >= a.C4;
+        if (bad4) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
+        dead[i] = __ballot_sync(0xFFFFFFFFu, !use || bad4);
+        sm.ks[st][o] = use ? fabsf(ks) : 0.f;
+        sm.vs[st][o] = use ? vs : 0.f;
+        if (use) top = max(top, __float_as_int(vs) >> 23);
       }
-      // K: a lane a token's chunk of 32 codes; 8 (16) tokens x 4 (2) chunks a warp: no bank conflicts
-      constexpr int CH = D / 32, CW = CH < 4 ? CH : 4, TW = 32 / CW;
+      top = __reduce_max_sync(0xFFFFFFFFu, top);
+      if (lane == 0) {
+        sm.v_exp[st] = top;
+        sm.dead[st] = static_cast<uint64_t>(dead[1]) << 32 | dead[0];
+      }
+      __syncwarp();
+      if (lane == 0) { mbar_arrive(&sm.sc_full[st]); mbar_arrive(&sm.raw_empty[rs]); }
+    }
+  } else if (warp >= H::SOFT) {
+    // ------------------------------------------------------------ unpackers
+    const int ut = tid - 32 * H::SOFT, uw = warp - H::SOFT;
+    // K: a lane a token's chunk of 32 codes; 8 (16) tokens x 4 (2) chunks a warp and step: no bank conflicts
+    constexpr int CH = D / 32, CW = CH < 4 ? CH : 4, TW = 32 / CW, STEPS = PT * CH / (32 * H::UNPACK);
+    const int e = lane & 7, dg = ut >> 3;  // V: a lane 8 dimensions of 8 tokens
+    for (int pg = 0; pg < n; ++pg) {
+      const int rs = pg % NRAW, st = pg % NST;
+      bool ok = pg < NST || wait(&sm.v_empty[st], pg / NST - 1);  // (the products of K end before those of V)
+      ok = ok && wait(&sm.raw_full[rs], pg / NRAW);
+      if (!__all_sync(0xFFFFFFFFu, ok)) break;
+      const uint8_t* src = raw + rs * p.raw_bytes;
+      const uint32_t kt = smem_u32(k_tile + st * H::TILE), vt = smem_u32(v_tile + st * H::TILE);
+      const int page = sm.page[rs];
+      uint64_t four = 0;  // tokens kept at 4 bits
+      if (page < 0) {     // nothing there
+        for (int i = ut; i < H::TILE / 16; i += 32 * H::UNPACK) st_shared_v4(kt + 16 * i, 0u, 0u, 0u, 0u);
+      } else {
 #pragma unroll
-      for (int it = 0; it < PT * CH / (32 * H::UNPACK); ++it) {
-        const int step = it * H::UNPACK + uw;
-        const int o = step / (CH / CW) * TW + lane % TW, c = step % (CH / CW) * CW + lane / TW;
-        uint32_t x[16];
-        if (page >= 0) {
+        for (int it = 0; it < STEPS; ++it) {
+          const int step = it * H::UNPACK + uw;
+          const int o = step / (CH / CW) * TW + lane % TW, c = step % (CH / CW) * CW + lane / TW;
           const uint32_t* w = reinterpret_cast<const uint32_t*>(src + o * RB + 12 * c);
           const uint32_t X[3] = {w[0], w[1], w[2]};
+          const uint32_t dst = kt + (c >> 1) * (PT * 128) + o * 128;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = k_operand(X, pair32(i));
-          if (a.C4 > 0 && o < live && signbit(scales[o]) && src[o * RB] < a.C4) {
-            const uint32_t* r4 = reinterpret_cast<const uint32_t*>(row4(src[o * RB]) + 16 * c);
-            const uint32_t y[4] = {r4[0], r4[1], r4[2], r4[3]};
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const Pair pr = pair32(i);
-              x[i] = four_bits(y[pr.lo >> 3] >> (4 * (pr.lo & 7)), 3 * pr.lo - pr.n) |
-                     four_bits(y[pr.hi >> 3] >> (4 * (pr.hi & 7)), 3 * pr.hi - pr.n - 16) << 16;
-            }
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = 0u;
+          for (int i = 0; i < 4; ++i)
+            st_shared_v4(dst + ((((c & 1) * 4 + i) ^ (o & 7)) << 4), k_operand(X, pair32(4 * i)), k_operand(X, pair32(4 * i + 1)),
+                         k_operand(X, pair32(4 * i + 2)), k_operand(X, pair32(4 * i + 3)));
         }
-        const uint32_t dst = smem_u32(k_tile + st * H::TILE) + (c >> 1) * (PT * 128) + o * 128;
+        if (a.C4 > 0) {
+          const float* scales = reinterpret_cast<const float*>(src + H::RAW_S);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) st_shared_v4(dst + ((((c & 1) * 4 + i) ^ (o & 7)) << 4), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+          for (int i = 0; i < 2; ++i) {
+            const int o = lane + 32 * i;
+            four |= static_cast<uint64_t>(__ballot_sync(0xFFFFFFFFu, signbit(scales[o]) && src[o * RB] < a.C4)) << (32 * i);
+          }
+          // their K rows, by the warp that has written what their 3-bit rows hold: lane i word i
+          __syncwarp();
+          for (uint64_t m = four; m; m &= m - 1) {
+            const int o = __ffsll(static_cast<long long>(m)) - 1, j = src[o * RB];
+            const uint8_t* r4 = p.c4_bytes ? src + H::RAW_4 + j * D : a.codes4 + ((static_cast<int64_t>(page) * a.H + h) * a.C4 + j) * D;
+#pragma unroll
+            for (int x = 0; x < CH / CW; ++x)
+              if ((o / TW * (CH / CW) + x) % H::UNPACK == uw)
+                for (int i = lane; i < 16 * CW; i += 32) {
+                  const int c = x * CW + (i >> 4), lo = kPairs[i & 15][0], hi = kPairs[i & 15][1];
+                  const uint8_t* y = r4 + 16 * c;
+                  const uint32_t v = four_bits((y[lo >> 1] >> (4 * (lo & 1)) & 15u) | (y[hi >> 1] >> (4 * (hi & 1)) & 15u) << 16,
+                                               kPairs[i & 15][2], kPairs[i & 15][3]);
+                  asm volatile("st.shared.u32 [%0], %1;" ::"r"(kt + (c >> 1) * (PT * 128) + o * 128 +
+                                                               ((((c & 1) * 4 + ((i & 15) >> 2)) ^ (o & 7)) << 4) + 4 * (i & 3)), "r"(v) : "memory");
+                }
+          }
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.k_full[st]);
-      // V: a lane 8 dimensions of 8 tokens
-      if (ut < D) {
-        const int e = lane & 7, dg = ut >> 3;
+      if (page < 0) {
+        for (int i = ut; i < H::TILE / 16; i += 32 * H::UNPACK) st_shared_v4(vt + 16 * i, 0u, 0u, 0u, 0u);
+      } else if (ut < D) {
         uint32_t x[8][4];
-        if (page >= 0) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const uint32_t* w = reinterpret_cast<const uint32_t*>(src + H::RAW_V + (2 * e + q) * GS + 12 * dg);
-            const uint32_t X[3] = {w[0], w[1], w[2]}, Y[3] = {X[0] >> 8, X[1] >> 8, X[2] >> 8};
-            v_operand<0>(X, Y, x[0][2 * q], x[0][2 * q + 1]);
-            v_operand<1>(X, Y, x[1][2 * q], x[1][2 * q + 1]);
-            v_operand<2>(X, Y, x[2][2 * q], x[2][2 * q + 1]);
-            v_operand<3>(X, Y, x[3][2 * q], x[3][2 * q + 1]);
-            v_operand<4>(X, Y, x[4][2 * q], x[4][2 * q + 1]);
-            v_operand<5>(X, Y, x[5][2 * q], x[5][2 * q + 1]);
-            v_operand<6>(X, Y, x[6][2 * q], x[6][2 * q + 1]);
-            v_operand<7>(X, Y, x[7][2 * q], x[7][2 * q + 1]);
-          }
-          if (a.C4 > 0) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int o = 8 * e + i;
-              if (o < live && signbit(scales[o]) && src[o * RB] < a.C4) {
-                const uint32_t y = *reinterpret_cast<const uint32_t*>(row4(src[o * RB]) + D / 2 + 4 * dg);
-#pragma unroll
-                for (int d = 0; d < 8; ++d) {  // token i: word 2 (i / 4) + i % 2, half i / 2 % 2
-                  uint32_t& z = x[d][2 * (i >> 2) + (i & 1)];
-                  const uint32_t v = four_bits(y >> (4 * d), v_bit(d));
-                  z = (i & 2) ? (z & 0xFFFFu) | v << 16 : (z & 0xFFFF0000u) | v;
-                }
-              }
-            }
-          }
-        } else {
-#pragma unroll
-          for (int d = 0; d < 8; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[d][i] = 0u;
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(src + H::RAW_V + (2 * e + q) * GS + 12 * dg);
+          const uint32_t X[3] = {w[0], w[1], w[2]}, Y[3] = {X[0] >> 8, X[1] >> 8, X[2] >> 8};
+          v_operand<0>(X, Y, x[0][2 * q], x[0][2 * q + 1]);
+          v_operand<1>(X, Y, x[1][2 * q], x[1][2 * q + 1]);
+          v_operand<2>(X, Y, x[2][2 * q], x[2][2 * q + 1]);
+          v_operand<3>(X, Y, x[3][2 * q], x[3][2 * q + 1]);
+          v_operand<4>(X, Y, x[4][2 * q], x[4][2 * q + 1]);
+          v_operand<5>(X, Y, x[5][2 * q], x[5][2 * q + 1]);
+          v_operand<6>(X, Y, x[6][2 * q], x[6][2 * q + 1]);
+          v_operand<7>(X, Y, x[7][2 * q], x[7][2 * q + 1]);
         }
-        const uint32_t dst = smem_u32(v_tile + st * H::TILE) + dg * 1024;
+        const uint32_t dst = vt + dg * 1024;
 #pragma unroll
         for (int d = 0; d < 8; ++d) st_shared_v4(dst + d * 128 + ((e ^ d) << 4), x[d][0], x[d][1], x[d][2], x[d][3]);
+        for (uint64_t m = four; m; m &= m - 1) {  // 4-bit tokens: token i of the 8 is word 2 (i / 4) + i % 2, half i / 2 % 2
+          const int o = __ffsll(static_cast<long long>(m)) - 1, j = src[o * RB];
+          if ((o >> 3) != e) continue;
+          const uint8_t* r4 = p.c4_bytes ? src + H::RAW_4 + j * D : a.codes4 + ((static_cast<int64_t>(page) * a.H + h) * a.C4 + j) * D;
+          const uint32_t y = *reinterpret_cast<const uint32_t*>(r4 + D / 2 + 4 * dg);
+          const int at = 4 * (2 * ((o >> 2) & 1) + (o & 1)) + (o & 2);
+#pragma unroll
+          for (int d = 0; d < 8; d += 2) {
+            const uint32_t v = four_bits((y >> (4 * d) & 15u) | (y >> (4 * d + 4) & 15u) << 16, v_bit(d), v_bit(d + 1));
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + d * 128 + ((e ^ d) << 4) + at), "h"(static_cast<uint16_t>(v)) : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(dst + (d + 1) * 128 + ((e ^ (d + 1)) << 4) + at), "h"(static_cast<uint16_t>(v >> 16)) : "memory");
+          }
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -347,10 +384,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     }
   } else {
     // -------------------------------------------------------------- softmax
-    const int t = warp >> 2, np = stream_pages(t);
+    const int t = warp >> 3, half = (warp >> 2) & 1, np = stream_pages(t);
     const int r0 = 128 * (tile0 + (pair ? t : 0)) + 32 * (warp & 3), r = r0 + lane;
-    float* out = p.parts + (static_cast<int64_t>(item) * STREAMS + t) * piece_floats(D, 128);
     const int col = 32 * (warp & 3) + lane;
+    float* out = p.parts + (static_cast<int64_t>(item) * STREAMS + t) * piece_floats(D, 128);
     if (r0 < rows) {
       const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
       const Segment sg{0, 0, rows, h, G, true};
@@ -369,44 +406,55 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         const float f = pow2_biased(fb);
         kq = a.qk_scale * 1.4426950408889634f * pow2_biased(263 - fb);
 #pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t x[32], y[32];
+        for (int c = half; c < D / 32; c += 2) {  // 32 dimensions
+          uint32_t x[16], y[16];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 v = q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q) + 8 * c + i) : make_uint4(0u, 0u, 0u, 0u);
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q) + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
             x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
           }
           auto qf = [&](int d) { return __uint_as_float((d & 1) ? (x[d >> 1] & 0xFFFF0000u) : (x[d >> 1] << 16)) * f; };
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const Pair pr = pair32(i & 15);
-            const int d0 = 32 * (i >> 4);
-            y[i] = pack_f16x2(qf(d0 + pr.lo) * (1.f / (1 << (3 * pr.lo - pr.n))), qf(d0 + pr.hi) * (1.f / (1 << (3 * pr.hi - pr.n - 16))));
+          for (int i = 0; i < 16; ++i) {
+            const Pair pr = pair32(i);
+            y[i] = pack_f16x2(qf(pr.lo) * (1.f / (1 << (3 * pr.lo - pr.n))), qf(pr.hi) * (1.f / (1 << (3 * pr.hi - pr.n - 16))));
           }
-          tmem_st32(tm + lanes + H::Q + t * (D / 2) + 32 * c, y);
+          if constexpr (H::QS) {
+            const uint32_t dst = smem_u32(q_tile + t * H::Q_TILE) + (c >> 1) * (128 * 128) + col * 128;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st_shared_v4(dst + ((((c & 1) * 4 + i) ^ (col & 7)) << 4), y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+          } else {
+            tmem_st16(tm + lanes + H::Q + t * (D / 2) + 16 * c, y);
+          }
         }
-        tmem_st_wait();
-        tc_fence_before();
+        if constexpr (H::QS) fence_proxy_async_smem();
+        else { tmem_st_wait(); tc_fence_before(); }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_full[t]);
       }
       const int n_all = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<unsigned>(max(sees, 0))) / PT);
       float ref = -INFINITY, l = 0.f;
       bool ok = true;
+      auto meet = [&](int k) {  // the two halves of 32 rows
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.meet[t][warp & 3]);
+        return __all_sync(0xFFFFFFFFu, wait(&sm.meet[t][warp & 3], k)) != 0;
+      };
       for (int k = 0; k < np; ++k) {
         const int pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
         const uint32_t s_col = tm + lanes + H::S + (t * SBUF + b) * PT;
         ok = wait(&sm.s_full[t][b], k / SBUF) && wait(&sm.sc_full[st], pg / NST);
         if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
         tc_fence_after();
-        float s[PT];
+        constexpr int HT = PT / 2;  // tokens HT half ..
+        float s[HT];
         {
-          uint32_t x[PT];
-          tmem_ld64(s_col, x);
+          uint32_t x[HT];
+          tmem_ld32(s_col + HT * half, x);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < PT; i += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(&sm.ks[st][i]);
+          for (int i = 0; i < HT; i += 4) {
+            const float4 ks = *reinterpret_cast<const float4*>(&sm.ks[st][HT * half + i]);
             const float2 u = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(ks.x, ks.y));
             const float2 v = mul2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(ks.z, ks.w));
             s[i] = u.x; s[i + 1] = u.y; s[i + 2] = v.x; s[i + 3] = v.y;
@@ -414,16 +462,23 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         }
         const uint64_t dead = sm.dead[st];
         if (pg >= n_all || dead != 0) {
-          const int lim = sees - pg * PT;
+          const int lim = sees - pg * PT - HT * half;
+          const uint32_t d = static_cast<uint32_t>(dead >> (HT * half));
 #pragma unroll
-          for (int i = 0; i < PT; ++i)
-            if (i >= lim || ((dead >> i) & 1)) s[i] = -INFINITY;
+          for (int i = 0; i < HT; ++i)
+            if (i >= lim || ((d >> i) & 1u)) s[i] = -INFINITY;
         }
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int i = 4; i < PT; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+        for (int i = 4; i < HT; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+        mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        sm.top[t][k & 1][half][col] = mx[0];
+        tc_fence_before();
+        if (!(ok = meet(k))) break;  // both halves have read S: P may go there
+        tc_fence_after();
+        mx[0] = fmaxf(mx[0], sm.top[t][k & 1][half ^ 1][col]);
         // weights stay below 2^15: p <= 2^8, V scales x 2^(133 - v_exp) below 2^7
-        const float want = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * kq + static_cast<float>(sm.v_exp[st] - 133);
+        const float want = mx[0] * kq + static_cast<float>(sm.v_exp[st] - 133);
         const bool grow = want > ref + 8.f || (ref == -INFINITY && want > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float now = grow ? want : ref;
@@ -433,7 +488,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
+            for (int c = half; c < D / 32; c += 2) {
               uint32_t x[32];
               tmem_ld32(tm + lanes + H::O + t * D + 32 * c, x);
               tmem_ld_wait();
@@ -449,10 +504,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         const float mr = ref == -INFINITY ? 0.f : ref;
         float sum[2] = {0.f, 0.f};
         // the words of P: V's order within 4 tokens is 0, 2, 1, 3
-        uint32_t w[PT / 2];
+        uint32_t w[HT / 2];
 #pragma unroll
-        for (int i = 0; i < PT; i += 4) {
-          const float4 vs = *reinterpret_cast<const float4*>(&sm.vs[st][i]);
+        for (int i = 0; i < HT; i += 4) {
+          const float4 vs = *reinterpret_cast<const float4*>(&sm.vs[st][HT * half + i]);
           float e[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -465,13 +520,13 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
           w[i / 2 + 1] = pack_f16x2(v.x, v.y);
         }
         l += sum[0] + sum[1];
-        tmem_st32(s_col, w);
+        tmem_st16(s_col + HT / 2 * half, w);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[t][b]);
       }
-      // ---- the piece
+      // ---- the piece: a half of the dimensions a thread
       if (ok && np > 0) {
         ok = wait(&sm.pv_done[t], np - 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -480,21 +535,21 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       if (ok) {
         if (np > 0)
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = half; c < D / 32; c += 2) {
             uint32_t x[32];
             tmem_ld32(tm + lanes + H::O + t * D + 32 * c, x);
             tmem_ld_wait();
             if (r < rows) {
               float4* dst = reinterpret_cast<float4*>(out + col * D + 32 * c);
+              auto o = [&](int i) { return __uint_as_float(x[i]) * (512.f / static_cast<float>(1 << v_bit(i & 7))); };
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                dst[i] = make_float4(__uint_as_float(x[4 * i]) * (512.f / (1 << v_bit((4 * i) & 7))), __uint_as_float(x[4 * i + 1]) * (512.f / (1 << v_bit((4 * i + 1) & 7))),
-                                     __uint_as_float(x[4 * i + 2]) * (512.f / (1 << v_bit((4 * i + 2) & 7))), __uint_as_float(x[4 * i + 3]) * (512.f / (1 << v_bit((4 * i + 3) & 7))));
+              for (int i = 0; i < 8; ++i) dst[i] = make_float4(o(4 * i), o(4 * i + 1), o(4 * i + 2), o(4 * i + 3));
             }
           }
-        if (r < rows) {
+        sm.top[t][np & 1][half][col] = l;
+        if (meet(np) && half == 0 && r < rows) {
           out[128 * D + col] = ref;
-          out[128 * D + 128 + col] = l;
+          out[128 * D + 128 + col] = l + sm.top[t][np & 1][1][col];
         }
       }
     }
@@ -515,7 +570,7 @@ cudaError_t launch_front_t(const AttnArgs& a, const FrontPlan& plan, float* part
   p.parts = parts;
   p.c4_bytes = a.C4 <= kStageRows4 ? a.C4 * D : 0;
   p.raw_bytes = H::RAW_4 + p.c4_bytes;
-  const int smem = 1024 + 2 * H::NST * H::TILE + H::NRAW * p.raw_bytes;
+  const int smem = 1024 + H::STREAMS * H::Q_TILE + 2 * H::NST * H::TILE + H::NRAW * p.raw_bytes;
   const cudaError_t e = set_smem_limit(front_kernel<D>, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(front_kernel<D>, dim3(static_cast<unsigned>(plan.items)), dim3(H::THREADS), smem, s, 0u, p);
