@@ -14,8 +14,7 @@
 //   issuer      one thread: S = Q K^T, O += P V (P in tensor memory where S
 //               was; two S a stream, so that the next one is there when a
 //               softmax ends)
-//   softmax     8 warps a stream, half a row's tokens a thread: s = S x (K
-//               scale), p = 2^(s - r), weights p x (V scale) rounded to fp16
+//   softmax     4 warps a stream, a row a thread: s = S x (K scale), p = 2^(s - r), weights p x (V scale) rounded to fp16
 //               (2^-11 of a weight, a quarter of what the output's rounding
 //               may take). r is the largest s so far plus the largest V scale's
 //               exponent; it moves, and O is multiplied, only when it grows by 8.
@@ -40,7 +39,7 @@ struct Shape {
   static constexpr bool QS = D == 128;               // Q in shared memory
   static constexpr int NST = D == 256 ? 2 : 4;       // K and V tiles
   static constexpr int NRAW = 3;                     // blocks as they come
-  static constexpr int SOFT = 8 * STREAMS, UNPACK = D == 256 ? 8 : 4;  // warps
+  static constexpr int SOFT = 4 * STREAMS, UNPACK = D == 256 ? 8 : 4;  // warps
   static constexpr int LOADER = SOFT + UNPACK, SCALER = LOADER + 1, ISSUER = SCALER + 1, THREADS = 32 * (ISSUER + 1);
   static constexpr int RB = row_bytes(D), GS = 4 * RB + 16;  // GS: stride of V's groups of 4 tokens
   static constexpr int RAW_V = PT * RB, RAW_S = RAW_V + 16 * GS, RAW_4 = RAW_S + 8 * PT;
@@ -56,11 +55,10 @@ struct Shared {
   uint64_t dead[H::NST];  // tokens that take no part
   int v_exp[H::NST];      // biased exponent of the largest V scale
   int page[H::NRAW];
-  uint64_t raw_full[H::NRAW], raw_empty[H::NRAW], k_full[H::NST], v_full[H::NST], v_empty[H::NST], sc_full[H::NST];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], meet[2][4], drain;
+  uint64_t raw_full[H::NRAW], raw_empty[H::NRAW], k_full[H::NST], v_full[H::NST], v_empty[H::NST];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], drain;
   uint32_t tmem;
   int abort;
-  float top[2][2][2][128];  // [stream][page's parity][half]: a row's largest score of a half
 };
 
 // D[tmem] (+)= A[tmem] B[smem]^T, fp16 x fp16 -> fp32
@@ -89,7 +87,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+// A 128-byte swizzled K-major operand's descriptor `words` 16-byte units behind
+// the one whose lower half is lo (the upper half has no address in it): one
+// addition an MMA, the issuing thread being the only one that can feed the tensor cores.
+__device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t words) {
+  constexpr uint32_t hi = (1024u >> 4) | 1u << 14 | 2u << 29;
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo + words), "r"(hi));
+  return d;
+}
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | 1u << 16; }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 // two codes of a 4-bit row (in the low nibbles of the halves) as fp16 (c - 8) 2^(j - 9): exact
 __device__ __forceinline__ uint32_t four_bits(uint32_t x, int jl, int jh) {
@@ -144,16 +157,14 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
   if (tid == 0) {
     for (int i = 0; i < NRAW; ++i) { mbar_init(&sm.raw_full[i], 1); mbar_init(&sm.raw_empty[i], H::UNPACK + 1); }
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&sm.k_full[i], H::UNPACK);
+      mbar_init(&sm.k_full[i], H::UNPACK + 1);
       mbar_init(&sm.v_full[i], H::UNPACK); mbar_init(&sm.v_empty[i], 1);
-      mbar_init(&sm.sc_full[i], 1);
     }
     for (int t = 0; t < STREAMS; ++t) {
-      const int live = 2 * ((stream_rows(t) + 31) / 32);  // warps with rows
+      const int live = (stream_rows(t) + 31) / 32;  // warps with rows
       mbar_init(&sm.q_full[t], live);
       for (int b = 0; b < SBUF; ++b) { mbar_init(&sm.s_full[t][b], 1); mbar_init(&sm.p_full[t][b], live); }
       mbar_init(&sm.pv_done[t], 1);
-      for (int i = 0; i < 4; ++i) mbar_init(&sm.meet[t][i], 2);
     }
     mbar_init(&sm.drain, 1);
     sm.abort = 0;
@@ -205,17 +216,18 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
   } else if (warp == H::ISSUER) {
     if (elect_one()) {
       constexpr uint32_t idS = make_idesc(1, 0, 0, 128, PT), idO = make_idesc(1, 0, 0, 128, D);
+      const uint32_t q_lo = desc_lo(smem_u32(q_tile)), k_lo = desc_lo(smem_u32(k_tile)), v_lo = desc_lo(smem_u32(v_tile));
       int n_s[2] = {0, 0};
       bool ok = true;
       auto issue_s = [&](int t) {
         const int k = n_s[t]++, pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
         if ((alternate || t == 0) && !(ok = wait(&sm.k_full[st], pg / NST))) return;
         tc_fence_after();
-        const uint32_t kt = smem_u32(k_tile + st * H::TILE), d = tm + H::S + (t * SBUF + b) * PT;
+        const uint32_t kt = k_lo + st * (H::TILE >> 4), d = tm + H::S + (t * SBUF + b) * PT, qt = q_lo + t * (H::Q_TILE >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          const uint64_t bd = smem_desc_sw128(kt + (i >> 2) * (PT * 128) + (i & 3) * 32);
-          if constexpr (H::QS) mma_f16_ss(d, smem_desc_sw128(smem_u32(q_tile + t * H::Q_TILE) + (i >> 2) * (128 * 128) + (i & 3) * 32), bd, idS, i > 0);
+          const uint64_t bd = desc_at(kt, (i >> 2) * (PT * 8) + (i & 3) * 2);
+          if constexpr (H::QS) mma_f16_ss(d, desc_at(qt, (i >> 2) * (128 * 8) + (i & 3) * 2), bd, idS, i > 0);
           else mma_f16_ts(d, tm + H::Q + t * (D / 2) + 8 * i, bd, idS, i > 0);
         }
         tc_commit(&sm.s_full[t][b]);
@@ -233,10 +245,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
           if (alternate || t == 0) ok = wait(&sm.v_full[st], pg / NST);
           if (!(ok = ok && wait(&sm.p_full[t][b], k / SBUF))) break;
           tc_fence_after();
-          const uint32_t vt = smem_u32(v_tile + st * H::TILE);
+          const uint32_t vt = v_lo + st * (H::TILE >> 4);
 #pragma unroll
           for (int i = 0; i < PT / 16; ++i)
-            mma_f16_ts(tm + H::O + t * D, tm + H::S + (t * SBUF + b) * PT + 8 * i, smem_desc_sw128(vt + i * 32), idO, k > 0 || i > 0);
+            mma_f16_ts(tm + H::O + t * D, tm + H::S + (t * SBUF + b) * PT + 8 * i, desc_at(vt, 2 * i), idO, k > 0 || i > 0);
           tc_commit(&sm.pv_done[t]);
           if (alternate || t == STREAMS - 1) tc_commit(&sm.v_empty[st]);
           if (n_s[t] < stream_pages(t)) issue_s(t);
@@ -283,7 +295,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         sm.dead[st] = static_cast<uint64_t>(dead[1]) << 32 | dead[0];
       }
       __syncwarp();
-      if (lane == 0) { mbar_arrive(&sm.sc_full[st]); mbar_arrive(&sm.raw_empty[rs]); }
+      if (lane == 0) { mbar_arrive(&sm.k_full[st]); mbar_arrive(&sm.raw_empty[rs]); }
     }
   } else if (warp >= H::SOFT) {
     // ------------------------------------------------------------ unpackers
@@ -384,7 +396,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     }
   } else {
     // -------------------------------------------------------------- softmax
-    const int t = warp >> 3, half = (warp >> 2) & 1, np = stream_pages(t);
+    const int t = warp >> 2, np = stream_pages(t);
     const int r0 = 128 * (tile0 + (pair ? t : 0)) + 32 * (warp & 3), r = r0 + lane;
     const int col = 32 * (warp & 3) + lane;
     float* out = p.parts + (static_cast<int64_t>(item) * STREAMS + t) * piece_floats(D, 128);
@@ -406,7 +418,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         const float f = pow2_biased(fb);
         kq = a.qk_scale * 1.4426950408889634f * pow2_biased(263 - fb);
 #pragma unroll 1
-        for (int c = half; c < D / 32; c += 2) {  // 32 dimensions
+        for (int c = 0; c < D / 32; ++c) {  // 32 dimensions
           uint32_t x[16], y[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -435,48 +447,37 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       const int n_all = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<unsigned>(max(sees, 0))) / PT);
       float ref = -INFINITY, l = 0.f;
       bool ok = true;
-      auto meet = [&](int k) {  // the two halves of 32 rows
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.meet[t][warp & 3]);
-        return __all_sync(0xFFFFFFFFu, wait(&sm.meet[t][warp & 3], k)) != 0;
-      };
       for (int k = 0; k < np; ++k) {
         const int pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
         const uint32_t s_col = tm + lanes + H::S + (t * SBUF + b) * PT;
-        ok = wait(&sm.s_full[t][b], k / SBUF) && wait(&sm.sc_full[st], pg / NST);
+        ok = wait(&sm.s_full[t][b], k / SBUF);  // (the page's scales were there before S was begun)
         if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
         tc_fence_after();
-        constexpr int HT = PT / 2;  // tokens HT half ..
-        float s[HT];
+        float2 s[PT / 2];
         {
-          uint32_t x[HT];
-          tmem_ld32(s_col + HT * half, x);
+          uint32_t x[PT];
+          tmem_ld64(s_col, x);
           tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < HT; i += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(&sm.ks[st][HT * half + i]);
-            const float2 u = mul2(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(ks.x, ks.y));
-            const float2 v = mul2(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(ks.z, ks.w));
-            s[i] = u.x; s[i + 1] = u.y; s[i + 2] = v.x; s[i + 3] = v.y;
+          for (int i = 0; i < PT; i += 4) {
+            const float4 ks = *reinterpret_cast<const float4*>(&sm.ks[st][i]);
+            s[i / 2] = __fmul2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), make_float2(ks.x, ks.y));
+            s[i / 2 + 1] = __fmul2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(ks.z, ks.w));
           }
         }
         const uint64_t dead = sm.dead[st];
         if (pg >= n_all || dead != 0) {
-          const int lim = sees - pg * PT - HT * half;
-          const uint32_t d = static_cast<uint32_t>(dead >> (HT * half));
+          const int lim = sees - pg * PT;
 #pragma unroll
-          for (int i = 0; i < HT; ++i)
-            if (i >= lim || ((d >> i) & 1u)) s[i] = -INFINITY;
+          for (int i = 0; i < PT; i += 2) {
+            if (i >= lim || ((dead >> i) & 1)) s[i / 2].x = -INFINITY;
+            if (i + 1 >= lim || ((dead >> (i + 1)) & 1)) s[i / 2].y = -INFINITY;
+          }
         }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int i = 4; i < HT; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-        mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        sm.top[t][k & 1][half][col] = mx[0];
-        tc_fence_before();
-        if (!(ok = meet(k))) break;  // both halves have read S: P may go there
-        tc_fence_after();
-        mx[0] = fmaxf(mx[0], sm.top[t][k & 1][half ^ 1][col]);
+        for (int i = 0; i < PT / 2; ++i) mx[i & 3] = max3(mx[i & 3], s[i].x, s[i].y);
+        mx[0] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         // weights stay below 2^15: p <= 2^8, V scales x 2^(133 - v_exp) below 2^7
         const float want = mx[0] * kq + static_cast<float>(sm.v_exp[st] - 133);
         const bool grow = want > ref + 8.f || (ref == -INFINITY && want > -INFINITY);
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             tc_fence_after();
 #pragma unroll 1
-            for (int c = half; c < D / 32; c += 2) {
+            for (int c = 0; c < D / 32; ++c) {
               uint32_t x[32];
               tmem_ld32(tm + lanes + H::O + t * D + 32 * c, x);
               tmem_ld_wait();
@@ -502,31 +503,31 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
           ref = now;
         }
         const float mr = ref == -INFINITY ? 0.f : ref;
-        float sum[2] = {0.f, 0.f};
+        const float2 kq2 = make_float2(kq, kq), mr2 = make_float2(-mr, -mr);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         // the words of P: V's order within 4 tokens is 0, 2, 1, 3
-        uint32_t w[HT / 2];
+        uint32_t w[PT / 2];
 #pragma unroll
-        for (int i = 0; i < HT; i += 4) {
-          const float4 vs = *reinterpret_cast<const float4*>(&sm.vs[st][HT * half + i]);
-          float e[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            e[c] = ex2(fmaf(s[i + c], kq, -mr));
-            sum[c & 1] += e[c];
-          }
-          const float2 u = mul2(make_float2(e[0], e[2]), make_float2(vs.x, vs.z));
-          const float2 v = mul2(make_float2(e[1], e[3]), make_float2(vs.y, vs.w));
-          w[i / 2] = pack_f16x2(u.x, u.y);
-          w[i / 2 + 1] = pack_f16x2(v.x, v.y);
+        for (int i = 0; i < PT; i += 4) {
+          const float4 vs = *reinterpret_cast<const float4*>(&sm.vs[st][i]);
+          float2 u = __ffma2_rn(s[i / 2], kq2, mr2), v = __ffma2_rn(s[i / 2 + 1], kq2, mr2);
+          u = make_float2(ex2(u.x), ex2(u.y));
+          v = make_float2(ex2(v.x), ex2(v.y));
+          sum[0] = __fadd2_rn(sum[0], u);
+          sum[1] = __fadd2_rn(sum[1], v);
+          u = __fmul2_rn(u, make_float2(vs.x, vs.y));
+          v = __fmul2_rn(v, make_float2(vs.z, vs.w));
+          w[i / 2] = pack_f16x2(u.x, v.x);
+          w[i / 2 + 1] = pack_f16x2(u.y, v.y);
         }
-        l += sum[0] + sum[1];
-        tmem_st16(s_col + HT / 2 * half, w);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        tmem_st32(s_col, w);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.p_full[t][b]);
       }
-      // ---- the piece: a half of the dimensions a thread
+      // ---- the piece
       if (ok && np > 0) {
         ok = wait(&sm.pv_done[t], np - 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       if (ok) {
         if (np > 0)
 #pragma unroll 1
-          for (int c = half; c < D / 32; c += 2) {
+          for (int c = 0; c < D / 32; ++c) {
             uint32_t x[32];
             tmem_ld32(tm + lanes + H::O + t * D + 32 * c, x);
             tmem_ld_wait();
@@ -546,10 +547,9 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
               for (int i = 0; i < 8; ++i) dst[i] = make_float4(o(4 * i), o(4 * i + 1), o(4 * i + 2), o(4 * i + 3));
             }
           }
-        sm.top[t][np & 1][half][col] = l;
-        if (meet(np) && half == 0 && r < rows) {
+        if (r < rows) {
           out[128 * D + col] = ref;
-          out[128 * D + 128 + col] = l + sm.top[t][np & 1][1][col];
+          out[128 * D + 128 + col] = l;
         }
       }
     }
