@@ -35,8 +35,8 @@ namespace {
 template <int D>
 struct Shape {
   static constexpr int STREAMS = front_streams(D);
-  static constexpr int SBUF = 2;                     // S buffers of a stream
-  static constexpr bool QS = D == 128;               // Q in shared memory
+  static constexpr int SBUF = D == 128 ? 1 : 2;      // S buffers of a stream
+  static constexpr bool QS = false;                  // Q in shared memory
   static constexpr int NST = D == 256 ? 2 : 4;       // K and V tiles
   static constexpr int NRAW = 3;                     // blocks as they come
   static constexpr int SOFT = 4 * STREAMS, UNPACK = D == 256 ? 8 : 4;  // warps
@@ -97,6 +97,13 @@ __device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t words) {
   return d;
 }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | 1u << 16; }
+
+// 0, but the compiler does not know: what follows from it stays out of the uniform registers and their pipe
+__device__ __forceinline__ int opaque_zero() {
+  int z;
+  asm volatile("mov.u32 %0, 0;" : "=r"(z));
+  return z;
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -214,15 +221,18 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     if (*abort)  // copies in flight land before the memory is released
       for (int i = max(0, put - NRAW); i < put; ++i) mbar_wait(&sm.raw_full[i % NRAW], (i / NRAW) & 1, a.timeout_ns, nullptr);
   } else if (warp == H::ISSUER) {
-    if (elect_one()) {
-      constexpr uint32_t idS = make_idesc(1, 0, 0, 128, PT), idO = make_idesc(1, 0, 0, 128, D);
-      const uint32_t q_lo = desc_lo(smem_u32(q_tile)), k_lo = desc_lo(smem_u32(k_tile)), v_lo = desc_lo(smem_u32(v_tile));
-      int n_s[2] = {0, 0};
-      bool ok = true;
-      auto issue_s = [&](int t) {
-        const int k = n_s[t]++, pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
-        if ((alternate || t == 0) && !(ok = wait(&sm.k_full[st], pg / NST))) return;
-        tc_fence_after();
+    // the warp stays together in the waits; one lane issues
+    constexpr uint32_t idS = make_idesc(1, 0, 0, 128, PT), idO = make_idesc(1, 0, 0, 128, D);
+    const uint32_t q_lo = desc_lo(smem_u32(q_tile)), k_lo = desc_lo(smem_u32(k_tile)), v_lo = desc_lo(smem_u32(v_tile));
+    const bool lead = elect_one() != 0;
+    int n_s[2] = {0, 0};
+    bool ok = true;
+    auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
+    auto issue_s = [&](int t) {
+      const int k = n_s[t]++, pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
+      if ((alternate || t == 0) && !(ok = wait_all(&sm.k_full[st], pg / NST))) return;
+      tc_fence_after();
+      if (lead) {
         const uint32_t kt = k_lo + st * (H::TILE >> 4), d = tm + H::S + (t * SBUF + b) * PT, qt = q_lo + t * (H::Q_TILE >> 4);
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
@@ -231,32 +241,36 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
           else mma_f16_ts(d, tm + H::Q + t * (D / 2) + 8 * i, bd, idS, i > 0);
         }
         tc_commit(&sm.s_full[t][b]);
-      };
-      for (int t = 0; t < STREAMS && ok; ++t)
-        if (stream_pages(t) > 0) ok = wait(&sm.q_full[t], 0);
-      tc_fence_after();
-      for (int b = 0; b < SBUF; ++b)
-        for (int t = 0; t < STREAMS; ++t)
-          if (ok && b < stream_pages(t)) issue_s(t);
-      for (int k = 0; k < stream_pages(0) && ok; ++k)
-        for (int t = 0; t < STREAMS; ++t) {
-          if (!ok || k >= stream_pages(t)) continue;
-          const int pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
-          if (alternate || t == 0) ok = wait(&sm.v_full[st], pg / NST);
-          if (!(ok = ok && wait(&sm.p_full[t][b], k / SBUF))) break;
-          tc_fence_after();
+      }
+      __syncwarp();
+    };
+    for (int t = 0; t < STREAMS && ok; ++t)
+      if (stream_pages(t) > 0) ok = wait_all(&sm.q_full[t], 0);
+    tc_fence_after();
+    for (int b = 0; b < SBUF; ++b)
+      for (int t = 0; t < STREAMS; ++t)
+        if (ok && b < stream_pages(t)) issue_s(t);
+    for (int k = 0; k < stream_pages(0) && ok; ++k)
+      for (int t = 0; t < STREAMS; ++t) {
+        if (!ok || k >= stream_pages(t)) continue;
+        const int pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
+        if (alternate || t == 0) ok = wait_all(&sm.v_full[st], pg / NST);
+        if (!(ok = ok && wait_all(&sm.p_full[t][b], k / SBUF))) break;
+        tc_fence_after();
+        if (lead) {
           const uint32_t vt = v_lo + st * (H::TILE >> 4);
 #pragma unroll
           for (int i = 0; i < PT / 16; ++i)
             mma_f16_ts(tm + H::O + t * D, tm + H::S + (t * SBUF + b) * PT + 8 * i, desc_at(vt, 2 * i), idO, k > 0 || i > 0);
           tc_commit(&sm.pv_done[t]);
           if (alternate || t == STREAMS - 1) tc_commit(&sm.v_empty[st]);
-          if (n_s[t] < stream_pages(t)) issue_s(t);
         }
-      if (!ok) {  // what was issued ends before the memory is released
-        tc_commit(&sm.drain);
-        mbar_wait(&sm.drain, 0, a.timeout_ns, nullptr);
+        __syncwarp();
+        if (n_s[t] < stream_pages(t)) issue_s(t);
       }
+    if (!ok && lead) {  // what was issued ends before the memory is released
+      tc_commit(&sm.drain);
+      mbar_wait(&sm.drain, 0, a.timeout_ns, nullptr);
     }
     __syncwarp();
   } else if (warp == H::SCALER) {
@@ -303,7 +317,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     // K: a lane a token's chunk of 32 codes; 8 (16) tokens x 4 (2) chunks a warp and step: no bank conflicts
     constexpr int CH = D / 32, CW = CH < 4 ? CH : 4, TW = 32 / CW, STEPS = PT * CH / (32 * H::UNPACK);
     const int e = lane & 7, dg = ut >> 3;  // V: a lane 8 dimensions of 8 tokens
-    for (int pg = 0; pg < n; ++pg) {
+    for (int pg = opaque_zero(); pg < n; ++pg) {
       const int rs = pg % NRAW, st = pg % NST;
       bool ok = pg < NST || wait(&sm.v_empty[st], pg / NST - 1);  // (the products of K end before those of V)
       ok = ok && wait(&sm.raw_full[rs], pg / NRAW);
@@ -396,7 +410,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     }
   } else {
     // -------------------------------------------------------------- softmax
-    const int t = warp >> 2, np = stream_pages(t);
+    const int t = (warp >> 2) + opaque_zero(), np = stream_pages(t);
     const int r0 = 128 * (tile0 + (pair ? t : 0)) + 32 * (warp & 3), r = r0 + lane;
     const int col = 32 * (warp & 3) + lane;
     float* out = p.parts + (static_cast<int64_t>(item) * STREAMS + t) * piece_floats(D, 128);
@@ -444,10 +458,12 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_full[t]);
       }
-      const int n_all = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<unsigned>(max(sees, 0))) / PT);
+      // pages before n_all are seen whole by all rows that see anything (a slot of the batch without a
+      // request would send its warp through the masks on every page)
+      const int n_all = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, sees <= 0 ? 0x7FFFFFFFu : static_cast<unsigned>(sees)) / PT);
       float ref = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int k = 0; k < np; ++k) {
+      for (int k = opaque_zero(); k < np; ++k) {
         const int pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
         const uint32_t s_col = tm + lanes + H::S + (t * SBUF + b) * PT;
         ok = wait(&sm.s_full[t][b], k / SBUF);  // (the page's scales were there before S was begun)
@@ -468,10 +484,12 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         const uint64_t dead = sm.dead[st];
         if (pg >= n_all || dead != 0) {
           const int lim = sees - pg * PT;
+          const uint64_t on = ~dead & (lim >= PT ? ~0ull : lim <= 0 ? 0ull : (1ull << lim) - 1ull);
+          const uint32_t w[2] = {static_cast<uint32_t>(on), static_cast<uint32_t>(on >> 32)};
 #pragma unroll
           for (int i = 0; i < PT; i += 2) {
-            if (i >= lim || ((dead >> i) & 1)) s[i / 2].x = -INFINITY;
-            if (i + 1 >= lim || ((dead >> (i + 1)) & 1)) s[i / 2].y = -INFINITY;
+            if (!(w[i >> 5] & (1u << (i & 31)))) s[i / 2].x = -INFINITY;
+            if (!(w[i >> 5] & (2u << (i & 31)))) s[i / 2].y = -INFINITY;
           }
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -548,8 +566,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
             }
           }
         if (r < rows) {
-          out[128 * D + col] = ref;
-          out[128 * D + 128 + col] = l;
+          out[128 * D + col] = sees > 0 ? ref : -INFINITY;
+          out[128 * D + 128 + col] = sees > 0 ? l : 0.f;
         }
       }
     }
