@@ -6,8 +6,9 @@
 // two "streams": two tiles on the same pages (each page taken apart once for
 // both), or, where a head has an odd tile left, one tile with its even and its
 // odd pages. With D = 256, tensor memory holds one stream.
-//   loader      one warp, bulk copies of a page's block into a ring (V's 16
-//               groups 16 bytes further apart, against bank conflicts)
+//   loader      one warp, a bulk copy of a page's block into a ring (V's 16
+//               groups one by one, further apart against bank conflicts, took
+//               1900 clocks a page: about 100 a copy, however small)
 //   unpackers   K -> [64 tokens][D], V -> [D][64 tokens] as fp16 codes - 4,
 //               128-byte swizzled; a token kept at 4 bits is one of these rows
 //   scaler      one warp, the scales beside them, and which tokens take part
@@ -38,11 +39,10 @@ struct Shape {
   static constexpr int SBUF = D == 128 ? 1 : 2;      // S buffers of a stream
   static constexpr bool QS = false;                  // Q in shared memory
   static constexpr int NST = D == 256 ? 2 : 4;       // K and V tiles
-  static constexpr int NRAW = 3;                     // blocks as they come
+  static constexpr int NRAW = D == 256 ? 3 : 4;      // blocks as they come
   static constexpr int SOFT = 4 * STREAMS, UNPACK = D == 256 ? 8 : 4;  // warps
   static constexpr int LOADER = SOFT + UNPACK, SCALER = LOADER + 1, ISSUER = SCALER + 1, THREADS = 32 * (ISSUER + 1);
-  static constexpr int RB = row_bytes(D), GS = 4 * RB + 16;  // GS: stride of V's groups of 4 tokens
-  static constexpr int RAW_V = PT * RB, RAW_S = RAW_V + 16 * GS, RAW_4 = RAW_S + 8 * PT;
+  static constexpr int RB = row_bytes(D);
   static constexpr int TILE = PT * D * 2, Q_TILE = QS ? 128 * D * 2 : 0;
   static constexpr int O = 0, Q = STREAMS * D, S = Q + (QS ? 0 : STREAMS * (D / 2));  // tensor memory columns
   static_assert(S + STREAMS * SBUF * PT <= 512);
@@ -129,7 +129,7 @@ __constant__ uint8_t kPairs[16][4] = {  // pair32's codes and their bits in the 
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __grid_constant__ FrontArgs p) {
   using H = Shape<D>;
-  constexpr int STREAMS = H::STREAMS, SBUF = H::SBUF, NST = H::NST, NRAW = H::NRAW, RB = H::RB, GS = H::GS;
+  constexpr int STREAMS = H::STREAMS, SBUF = H::SBUF, NST = H::NST, NRAW = H::NRAW, RB = H::RB;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared<D> sm;
   const AttnArgs& a = p.a;
@@ -210,12 +210,9 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       __syncwarp();
       if (good) {
         const int64_t at = static_cast<int64_t>(page) * a.H + h;
-        const uint8_t* blk = a.pages + at * block_bytes(D);
         uint8_t* dst = raw + st * p.raw_bytes;
-        if (lane < 16) bulk_load(dst + H::RAW_V + lane * GS, blk + off_v(D) + lane * 4 * RB, 4 * RB, &sm.raw_full[st]);
-        else if (lane == 16) bulk_load(dst, blk, PT * RB, &sm.raw_full[st]);
-        else if (lane == 17) bulk_load(dst + H::RAW_S, blk + off_ks(D), 8 * PT, &sm.raw_full[st]);
-        else if (lane == 18 && c4_bytes) bulk_load(dst + H::RAW_4, a.codes4 + at * c4_bytes, c4_bytes, &sm.raw_full[st]);
+        if (lane == 0) bulk_load(dst, a.pages + at * block_bytes(D), block_bytes(D), &sm.raw_full[st]);
+        else if (lane == 1 && c4_bytes) bulk_load(dst + block_bytes(D), a.codes4 + at * c4_bytes, c4_bytes, &sm.raw_full[st]);
       }
     }
     if (*abort)  // copies in flight land before the memory is released
@@ -287,7 +284,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       ok = ok && wait(&sm.raw_full[rs], pg / NRAW);
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       const uint8_t* src = raw + rs * p.raw_bytes;
-      const float* scales = reinterpret_cast<const float*>(src + H::RAW_S);
+      const float* scales = reinterpret_cast<const float*>(src + off_ks(D));
       const int live = sm.page[rs] < 0 ? 0 : min(PT, seen - (first + pg) * PT);
       uint32_t dead[2];
       int top = 14;
@@ -317,32 +314,56 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     // K: a lane a token's chunk of 32 codes; 8 (16) tokens x 4 (2) chunks a warp and step: no bank conflicts
     constexpr int CH = D / 32, CW = CH < 4 ? CH : 4, TW = 32 / CW, STEPS = PT * CH / (32 * H::UNPACK);
     const int e = lane & 7, dg = ut >> 3;  // V: a lane 8 dimensions of 8 tokens
-    for (int pg = opaque_zero(); pg < n; ++pg) {
+    // the words of a page, taken while the page before it is worked on
+    uint32_t kw[STEPS][3], vw[2][3];
+    int page = -1;
+    auto take = [&](int pg) {
+      const int rs = pg % NRAW;
+      if (!__all_sync(0xFFFFFFFFu, wait(&sm.raw_full[rs], pg / NRAW))) return false;
+      const uint8_t* src = raw + rs * p.raw_bytes;
+      page = sm.page[rs];
+#pragma unroll
+      for (int it = 0; it < STEPS; ++it) {
+        const int step = it * H::UNPACK + uw;
+        const int o = step / (CH / CW) * TW + lane % TW, c = step % (CH / CW) * CW + lane / TW;
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(src + o * RB + 12 * c);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) kw[it][i] = w[i];
+      }
+      if (ut < D) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(src + off_v(D) + (2 * e + q) * 4 * RB + 12 * dg);
+#pragma unroll
+          for (int i = 0; i < 3; ++i) vw[q][i] = w[i];
+        }
+      }
+      return true;
+    };
+    bool ok = n > 0 && take(0);
+    for (int pg = 0; pg < n && ok; ++pg) {
       const int rs = pg % NRAW, st = pg % NST;
-      bool ok = pg < NST || wait(&sm.v_empty[st], pg / NST - 1);  // (the products of K end before those of V)
-      ok = ok && wait(&sm.raw_full[rs], pg / NRAW);
+      ok = pg < NST || wait(&sm.v_empty[st], pg / NST - 1);  // (the products of K end before those of V)
       if (!__all_sync(0xFFFFFFFFu, ok)) break;
       const uint8_t* src = raw + rs * p.raw_bytes;
       const uint32_t kt = smem_u32(k_tile + st * H::TILE), vt = smem_u32(v_tile + st * H::TILE);
-      const int page = sm.page[rs];
+      const int now = page;
       uint64_t four = 0;  // tokens kept at 4 bits
-      if (page < 0) {     // nothing there
+      if (now < 0) {      // nothing there
         for (int i = ut; i < H::TILE / 16; i += 32 * H::UNPACK) st_shared_v4(kt + 16 * i, 0u, 0u, 0u, 0u);
       } else {
 #pragma unroll
         for (int it = 0; it < STEPS; ++it) {
           const int step = it * H::UNPACK + uw;
           const int o = step / (CH / CW) * TW + lane % TW, c = step % (CH / CW) * CW + lane / TW;
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(src + o * RB + 12 * c);
-          const uint32_t X[3] = {w[0], w[1], w[2]};
           const uint32_t dst = kt + (c >> 1) * (PT * 128) + o * 128;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            st_shared_v4(dst + ((((c & 1) * 4 + i) ^ (o & 7)) << 4), k_operand(X, pair32(4 * i)), k_operand(X, pair32(4 * i + 1)),
-                         k_operand(X, pair32(4 * i + 2)), k_operand(X, pair32(4 * i + 3)));
+            st_shared_v4(dst + ((((c & 1) * 4 + i) ^ (o & 7)) << 4), k_operand(kw[it], pair32(4 * i)), k_operand(kw[it], pair32(4 * i + 1)),
+                         k_operand(kw[it], pair32(4 * i + 2)), k_operand(kw[it], pair32(4 * i + 3)));
         }
         if (a.C4 > 0) {
-          const float* scales = reinterpret_cast<const float*>(src + H::RAW_S);
+          const float* scales = reinterpret_cast<const float*>(src + off_ks(D));
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int o = lane + 32 * i;
@@ -352,7 +373,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
           __syncwarp();
           for (uint64_t m = four; m; m &= m - 1) {
             const int o = __ffsll(static_cast<long long>(m)) - 1, j = src[o * RB];
-            const uint8_t* r4 = p.c4_bytes ? src + H::RAW_4 + j * D : a.codes4 + ((static_cast<int64_t>(page) * a.H + h) * a.C4 + j) * D;
+            const uint8_t* r4 = p.c4_bytes ? src + block_bytes(D) + j * D : a.codes4 + ((static_cast<int64_t>(now) * a.H + h) * a.C4 + j) * D;
 #pragma unroll
             for (int x = 0; x < CH / CW; ++x)
               if ((o / TW * (CH / CW) + x) % H::UNPACK == uw)
@@ -370,30 +391,31 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm.k_full[st]);
-      if (page < 0) {
+      uint32_t x[8][4];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t (&X)[3] = vw[q];
+        const uint32_t Y[3] = {X[0] >> 8, X[1] >> 8, X[2] >> 8};
+        v_operand<0>(X, Y, x[0][2 * q], x[0][2 * q + 1]);
+        v_operand<1>(X, Y, x[1][2 * q], x[1][2 * q + 1]);
+        v_operand<2>(X, Y, x[2][2 * q], x[2][2 * q + 1]);
+        v_operand<3>(X, Y, x[3][2 * q], x[3][2 * q + 1]);
+        v_operand<4>(X, Y, x[4][2 * q], x[4][2 * q + 1]);
+        v_operand<5>(X, Y, x[5][2 * q], x[5][2 * q + 1]);
+        v_operand<6>(X, Y, x[6][2 * q], x[6][2 * q + 1]);
+        v_operand<7>(X, Y, x[7][2 * q], x[7][2 * q + 1]);
+      }
+      if (pg + 1 < n) ok = take(pg + 1);
+      if (now < 0) {
         for (int i = ut; i < H::TILE / 16; i += 32 * H::UNPACK) st_shared_v4(vt + 16 * i, 0u, 0u, 0u, 0u);
       } else if (ut < D) {
-        uint32_t x[8][4];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(src + H::RAW_V + (2 * e + q) * GS + 12 * dg);
-          const uint32_t X[3] = {w[0], w[1], w[2]}, Y[3] = {X[0] >> 8, X[1] >> 8, X[2] >> 8};
-          v_operand<0>(X, Y, x[0][2 * q], x[0][2 * q + 1]);
-          v_operand<1>(X, Y, x[1][2 * q], x[1][2 * q + 1]);
-          v_operand<2>(X, Y, x[2][2 * q], x[2][2 * q + 1]);
-          v_operand<3>(X, Y, x[3][2 * q], x[3][2 * q + 1]);
-          v_operand<4>(X, Y, x[4][2 * q], x[4][2 * q + 1]);
-          v_operand<5>(X, Y, x[5][2 * q], x[5][2 * q + 1]);
-          v_operand<6>(X, Y, x[6][2 * q], x[6][2 * q + 1]);
-          v_operand<7>(X, Y, x[7][2 * q], x[7][2 * q + 1]);
-        }
         const uint32_t dst = vt + dg * 1024;
 #pragma unroll
         for (int d = 0; d < 8; ++d) st_shared_v4(dst + d * 128 + ((e ^ d) << 4), x[d][0], x[d][1], x[d][2], x[d][3]);
         for (uint64_t m = four; m; m &= m - 1) {  // 4-bit tokens: token i of the 8 is word 2 (i / 4) + i % 2, half i / 2 % 2
           const int o = __ffsll(static_cast<long long>(m)) - 1, j = src[o * RB];
           if ((o >> 3) != e) continue;
-          const uint8_t* r4 = p.c4_bytes ? src + H::RAW_4 + j * D : a.codes4 + ((static_cast<int64_t>(page) * a.H + h) * a.C4 + j) * D;
+          const uint8_t* r4 = p.c4_bytes ? src + block_bytes(D) + j * D : a.codes4 + ((static_cast<int64_t>(now) * a.H + h) * a.C4 + j) * D;
           const uint32_t y = *reinterpret_cast<const uint32_t*>(r4 + D / 2 + 4 * dg);
           const int at = 4 * (2 * ((o >> 2) & 1) + (o & 1)) + (o & 2);
 #pragma unroll
@@ -422,21 +444,27 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       if (np > 0) {  // the row's query: fp16, its largest value in [2^14, 2^15)
         const uint16_t* q = r < rows ? query_row(a, sg, r) : nullptr;
         uint32_t am = 0u;
-        if (q != nullptr)
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + i);
+        uint4 row[16];  // 128 dimensions, all of them where there are no more
+#pragma unroll
+        for (int c = 0; c < (D + 127) / 128; ++c) {
+#pragma unroll
+          for (int i = 0; i < (D < 128 ? D / 8 : 16); ++i) row[i] = q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q) + 16 * c + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+          for (int i = 0; i < (D < 128 ? D / 8 : 16); ++i) {
+            const uint4 v = row[i];
             am = max(am, max(max(max(v.x & 0x7FFFu, (v.x >> 16) & 0x7FFFu), max(v.y & 0x7FFFu, (v.y >> 16) & 0x7FFFu)),
                              max(max(v.z & 0x7FFFu, (v.z >> 16) & 0x7FFFu), max(v.w & 0x7FFFu, (v.w >> 16) & 0x7FFFu))));
           }
+        }
         const int fb = min(268 - max(1, static_cast<int>(am >> 7)), 254);
         const float f = pow2_biased(fb);
         kq = a.qk_scale * 1.4426950408889634f * pow2_biased(263 - fb);
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < D / 32; ++c) {  // 32 dimensions
           uint32_t x[16], y[16];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint4 v = q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q) + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 v = D <= 128 ? row[(4 * c + i) & 15] : q != nullptr ? __ldg(reinterpret_cast<const uint4*>(q) + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
             x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
           }
           auto qf = [&](int d) { return __uint_as_float((d & 1) ? (x[d >> 1] & 0xFFFF0000u) : (x[d >> 1] << 16)) * f; };
@@ -587,7 +615,7 @@ cudaError_t launch_front_t(const AttnArgs& a, const FrontPlan& plan, float* part
   p.plan = plan;
   p.parts = parts;
   p.c4_bytes = a.C4 <= kStageRows4 ? a.C4 * D : 0;
-  p.raw_bytes = H::RAW_4 + p.c4_bytes;
+  p.raw_bytes = block_bytes(D) + p.c4_bytes;
   const int smem = 1024 + H::STREAMS * H::Q_TILE + 2 * H::NST * H::TILE + H::NRAW * p.raw_bytes;
   const cudaError_t e = set_smem_limit(front_kernel<D>, smem);
   if (e != cudaSuccess) return e;
