@@ -60,7 +60,7 @@ struct Cursor {  // a unit: page j of P of segment seg = (b heads + h) groups + 
 
 // Page: the arithmetic on a page's block (paged_mma.cuh).
 template <int D, typename Page, int WARPS, int NS>
-__global__ void __launch_bounds__(32 * WARPS, 1) walk_kernel(const __grid_constant__ WalkArgs p) {
+__global__ void __launch_bounds__(32 * WARPS, 2) walk_kernel(const __grid_constant__ WalkArgs p) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t s_full[WARPS][NS];
   __shared__ int s_page[WARPS][NS];
@@ -372,16 +372,19 @@ struct Plan {
   int64_t off_front, off_cum, bytes;
 };
 
-constexpr int walk_warps(int D) { return D == 256 ? 8 : 16; }
+// Two CTAs an SM: of one walk, or one of each where both walks run (the second is launched behind the
+// first and runs beside it).
+constexpr int walk_warps(int D) { return D == 256 ? 4 : 8; }
 constexpr int walk_stages(int D) { return D == 64 ? 3 : 2; }
 
-static Plan::Walk plan_walk(int64_t D, int64_t rows, int64_t segs_per_group, int64_t max_units_per_group, bool any) {
+static Plan::Walk plan_walk(int64_t D, int64_t rows, int64_t segs_per_group, int64_t max_units_per_group, bool any, int per_sm) {
   Plan::Walk w{};
   w.cols = rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
   w.groups = static_cast<int>((rows + w.cols - 1) / w.cols);
   if (!any) return w;
   const int64_t units = max_units_per_group * w.groups;
-  w.grid = static_cast<int>(units < num_sms() ? units : num_sms());
+  const int64_t most = static_cast<int64_t>(per_sm) * num_sms();
+  w.grid = static_cast<int>(units < most ? units : most);
   w.nw = static_cast<int64_t>(w.grid) * walk_warps(static_cast<int>(D));
   w.slots = segs_per_group * w.groups + w.nw;
   return w;
@@ -406,15 +409,18 @@ static FrontPlan plan_tiles(int64_t D, int64_t rows, int64_t H, int64_t n) {
   return p;
 }
 
-constexpr int64_t kTileRows = 5;  // rows from which the tensor-core kernel takes the shared pages
+// Rows from which the tensor-core kernel takes the shared pages. Walk / tiles, whole call in us, D = 128:
+// 64 pages x 32 heads 8 rows 36 / 38, 16 rows 37 / 39, 32 rows 46 / 40; 256 pages x 8 heads 43 / 36, 42 / 36, 48 / 40.
+constexpr int64_t kTileRows = 17;
 
 static Plan make_plan(int64_t B, int64_t Sq, int64_t Hq, int64_t H, int64_t D, int64_t n_shared, int64_t W) {
   Plan p{};
   const int64_t rows = Sq * (Hq / H);
-  p.own = plan_walk(D, rows, B * H, B * W * H, W > 0);
   const bool tiled = n_shared > 0 && B * rows >= kTileRows;
+  const int per_sm = W > 0 && n_shared > 0 && !tiled ? 1 : 2;
+  p.own = plan_walk(D, rows, B * H, B * W * H, W > 0, per_sm);
   if (tiled) p.tiles = plan_tiles(D, B * rows, H, n_shared);
-  p.front = plan_walk(D, B * rows, H, n_shared * H, n_shared > 0 && !tiled);
+  p.front = plan_walk(D, B * rows, H, n_shared * H, n_shared > 0 && !tiled, per_sm);
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   p.off_front = up(p.own.slots * piece_floats(static_cast<int>(D), p.own.cols) * 4);
   p.off_cum = p.off_front + up(tiled ? p.tiles.items * front_streams(static_cast<int>(D)) * piece_floats(static_cast<int>(D), 128) * 4

@@ -314,6 +314,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     // K: a lane a token's chunk of 32 codes; 8 (16) tokens x 4 (2) chunks a warp and step: no bank conflicts
     constexpr int CH = D / 32, CW = CH < 4 ? CH : 4, TW = 32 / CW, STEPS = PT * CH / (32 * H::UNPACK);
     const int e = lane & 7, dg = ut >> 3;  // V: a lane 8 dimensions of 8 tokens
+    const int p_lo = kPairs[lane & 15][0], p_hi = kPairs[lane & 15][1], p_jl = kPairs[lane & 15][2], p_jh = kPairs[lane & 15][3];
     // the words of a page, taken while the page before it is worked on
     uint32_t kw[STEPS][3], vw[2][3];
     int page = -1;
@@ -377,13 +378,13 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
 #pragma unroll
             for (int x = 0; x < CH / CW; ++x)
               if ((o / TW * (CH / CW) + x) % H::UNPACK == uw)
-                for (int i = lane; i < 16 * CW; i += 32) {
-                  const int c = x * CW + (i >> 4), lo = kPairs[i & 15][0], hi = kPairs[i & 15][1];
+#pragma unroll
+                for (int i = 0; i < CW / 2; ++i) {
+                  const int c = x * CW + 2 * i + (lane >> 4);
                   const uint8_t* y = r4 + 16 * c;
-                  const uint32_t v = four_bits((y[lo >> 1] >> (4 * (lo & 1)) & 15u) | (y[hi >> 1] >> (4 * (hi & 1)) & 15u) << 16,
-                                               kPairs[i & 15][2], kPairs[i & 15][3]);
+                  const uint32_t v = four_bits((y[p_lo >> 1] >> (4 * (p_lo & 1)) & 15u) | (y[p_hi >> 1] >> (4 * (p_hi & 1)) & 15u) << 16, p_jl, p_jh);
                   asm volatile("st.shared.u32 [%0], %1;" ::"r"(kt + (c >> 1) * (PT * 128) + o * 128 +
-                                                               ((((c & 1) * 4 + ((i & 15) >> 2)) ^ (o & 7)) << 4) + 4 * (i & 3)), "r"(v) : "memory");
+                                                               ((((c & 1) * 4 + ((lane & 15) >> 2)) ^ (o & 7)) << 4) + 4 * (lane & 3)), "r"(v) : "memory");
                 }
           }
         }
