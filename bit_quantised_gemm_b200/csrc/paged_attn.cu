@@ -25,15 +25,16 @@ namespace blt {
 namespace paged {
 
 // --------------------------------------------------------------------- walk
-// A unit is (page, cache head, group of columns). The units of one (sequence,
-// head, group) lie side by side, warp w of NW takes the units
-// [U w / NW, U (w + 1) / NW): equal shares whatever the lengths are. Each warp
-// streams its pages' blocks (one bulk copy a block) through a ring of its own
-// and shares nothing with its neighbours.
+// The pages of one (sequence, head, group of columns) are a segment. Segments
+// lie one behind the other, each as long as its pages and kOverhead more (what
+// beginning and ending one costs, in pages: without it a warp among one-page
+// sequences took 27 segments where others took one), and warp w of NW takes
+// the pages that lie in [U w / NW, U (w + 1) / NW): equal shares whatever the
+// lengths are. Each warp streams its pages' blocks (one bulk copy a block)
+// through a ring of its own and shares nothing with its neighbours.
 //
-// Its piece of segment s = (sequence, head, group) goes to slot s + w: along
-// the units either s or w grows from one piece to the next, so no two pieces
-// have one slot.
+// Its piece of segment s goes to slot s + w: along the line either s or w
+// grows from one piece to the next, so no two pieces have one slot.
 
 struct WalkArgs {
   AttnArgs a;
@@ -42,11 +43,11 @@ struct WalkArgs {
   int stage_bytes;
   int late_wait;    // an earlier kernel of this call has waited for what the call depends on
   float* parts;     // pieces
-  int64_t* cum;     // [B + 1] own pages before sequence b (written)
+  int64_t* cum;     // [B + 1] length of one head's and group's segments before sequence b (written)
 };
 
 
-// warps that have units (each one at least), the first unit of warp w, and the warp that has unit u
+// warps with a share of a line of U (each one unit at least), where that of warp w begins, and the warp that has unit u
 __device__ __forceinline__ int64_t walkers(int64_t U, int64_t NW) { return U < NW ? U : NW; }
 __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {  // of numbers that are not negative
   return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
@@ -54,8 +55,8 @@ __device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {  // of numbers t
 __device__ __forceinline__ int64_t first_unit(int64_t U, int64_t w, int64_t NW) { return quot(U * w, NW); }
 __device__ __forceinline__ int64_t warp_of(int64_t U, int64_t u, int64_t NW) { return quot((u + 1) * NW - 1, U); }
 
-struct Cursor {  // a unit: page j of P of segment seg = (b heads + h) groups + group
-  int b, h, grp, j, P;
+struct Cursor {  // page j of P of a segment, at place x of the warp's share
+  int b, h, grp, j, P, x;
 };
 
 // Page: the arithmetic on a page's block (paged_mma.cuh).
@@ -66,6 +67,7 @@ __global__ void __launch_bounds__(32 * WARPS, 2) walk_kernel(const __grid_consta
   __shared__ int s_page[WARPS][NS];
   __shared__ int64_t s_cum[32 * WARPS + 1];
   __shared__ int64_t s_sum[WARPS];
+  constexpr int OV = segment_overhead(Page::COLS);
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (lane == 0) {
@@ -75,12 +77,12 @@ __global__ void __launch_bounds__(32 * WARPS, 2) walk_kernel(const __grid_consta
   if (!p.late_wait) pdl_wait();
   pdl_trigger();
 
-  // ---- units: pages before each chunk of sequences, then this warp's share
+  // ---- the line: its length before each chunk of sequences, then this warp's share
   const int chunk = (a.B + 32 * WARPS - 1) / (32 * WARPS);
   int64_t U;
   if (p.front) {
     __syncthreads();
-    U = static_cast<int64_t>(a.n_shared) * a.H * p.groups;
+    U = static_cast<int64_t>(a.n_shared + OV) * a.H * p.groups;
   } else {
     int64_t mine = 0;
     const int b0 = tid * chunk, b1 = min(a.B, b0 + chunk);
@@ -88,7 +90,8 @@ __global__ void __launch_bounds__(32 * WARPS, 2) walk_kernel(const __grid_consta
       bool bad;
       const int len = cut_len(a, b, &bad);
       if (bad && blockIdx.x == 0) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
-      mine += max(0, pages_of(len) - a.n_shared);
+      const int P = pages_of(len) - a.n_shared;
+      if (P > 0) mine += P + OV;
     }
     int64_t upto = mine;
 #pragma unroll
@@ -107,53 +110,63 @@ __global__ void __launch_bounds__(32 * WARPS, 2) walk_kernel(const __grid_consta
       int64_t c = upto - mine;
       for (int b = b0; b < b1; ++b) {
         p.cum[b] = c;
-        c += own_pages(a, b);
+        const int P = own_pages(a, b);
+        if (P > 0) c += P + OV;
       }
       if (tid == 0) p.cum[a.B] = s_cum[32 * WARPS];
     }
   }
-  // few units: one a warp, over all SMs (neighbouring numbers lie on neighbouring SMs)
+  // few pages: one a warp, over all SMs (neighbouring numbers lie on neighbouring SMs)
   const int64_t NW = walkers(U, static_cast<int64_t>(gridDim.x) * WARPS);
   const int64_t wid = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
-  const int64_t u0 = wid < NW ? first_unit(U, wid, NW) : 0;
-  const int n_units = wid < NW ? static_cast<int>(first_unit(U, wid + 1, NW) - u0) : 0;
-  if (n_units > 0) {
+  const int64_t x0 = wid < NW ? first_unit(U, wid, NW) : 0;
+  const int limit = wid < NW ? static_cast<int>(first_unit(U, wid + 1, NW) - x0) : 0;
+  if (limit > 0) {
     Cursor take;
     int64_t seg;
+    int off;  // place in the segment
+    const int64_t hg = static_cast<int64_t>(a.H) * p.groups;
     if (p.front) {
-      seg = quot(u0, a.n_shared);
+      seg = quot(x0, a.n_shared + OV);
       take.b = 0;
       take.P = a.n_shared;
-      take.j = static_cast<int>(u0 - seg * a.n_shared);
+      off = static_cast<int>(x0 - seg * (a.n_shared + OV));
       take.h = static_cast<int>(quot(seg, p.groups));
       take.grp = static_cast<int>(seg - static_cast<int64_t>(take.h) * p.groups);
     } else {
-      const int64_t hg = static_cast<int64_t>(a.H) * p.groups;
-      const int64_t pg = quot(u0, hg);
-      int lo = 0, hi = 32 * WARPS - 1;  // the last chunk that begins at or before pg
+      const int64_t at = quot(x0, hg);
+      int lo = 0, hi = 32 * WARPS - 1;  // the last chunk that begins at or before that
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (s_cum[mid] <= pg) lo = mid; else hi = mid - 1;
+        if (s_cum[mid] <= at) lo = mid; else hi = mid - 1;
       }
       int64_t c = s_cum[lo];
       int b = lo * chunk, P = own_pages(a, b);
-      while (c + P <= pg) { c += P; P = own_pages(a, ++b); }
-      const int64_t v = u0 - c * hg, s = quot(v, P);
+      while (P == 0 || c + P + OV <= at) {
+        if (P > 0) c += P + OV;
+        P = own_pages(a, ++b);
+      }
+      const int64_t v = x0 - c * hg, s = quot(v, P + OV);
       take.b = b;
       take.P = P;
-      take.j = static_cast<int>(v - s * P);
+      off = static_cast<int>(v - s * (P + OV));
       take.h = static_cast<int>(quot(s, p.groups));
       take.grp = static_cast<int>(s - static_cast<int64_t>(take.h) * p.groups);
       seg = static_cast<int64_t>(b) * hg + s;
     }
+    take.j = max(off - OV, 0);
+    take.x = max(OV - off, 0);
     auto advance = [&](Cursor& c) {
+      ++c.x;
       if (++c.j < c.P) return;
+      c.x += OV;
+      if (c.x >= limit) return;
       c.j = 0;
       if (++c.grp < p.groups) return;
       c.grp = 0;
       if (++c.h < a.H) return;
       c.h = 0;
-      do { c.P = own_pages(a, ++c.b); } while (c.P == 0);  // called only while units are left
+      do { c.P = own_pages(a, ++c.b); } while (c.P == 0);  // the line goes on: there is one
     };
 
     uint8_t* ring = smem + static_cast<size_t>(warp) * NS * p.stage_bytes;
@@ -185,22 +198,22 @@ __global__ void __launch_bounds__(32 * WARPS, 2) walk_kernel(const __grid_consta
         }
       }
       ++n_put;
-      if (n_put < n_units) advance(put);
+      advance(put);
     };
-    while (n_put < min(NS, n_units)) issue();
+    while (n_put < NS && put.x < limit) issue();
 
     const int G = a.Hq / a.H;
     const int rows = (p.front ? a.B : 1) * a.Sq * G;  // of a (sequence, head)
     uint32_t parity = 0u;                             // bit per stage
     int st = 0;
     bool ok = true;
-    for (int k = 0; k < n_units && ok;) {
+    while (take.x < limit && ok) {
       Segment sg{p.front ? 0 : take.b * a.Sq, take.grp * Page::COLS, rows, take.h, G, p.front != 0};
       float* out = p.parts + (seg + wid) * piece_floats(D, Page::COLS);
       Page pg;
       pg.begin(a, sg, out);
-      const int last = min(n_units - k, take.P - take.j);
-      for (int e = 0; e < last; ++e, ++k) {
+      const int last = min(limit - take.x, take.P - take.j);
+      for (int e = 0; e < last; ++e) {
         const uint8_t* blk = ring + st * p.stage_bytes;
         __syncwarp();  // s_page is lane 0's
         const int page = s_page[warp][st];
@@ -212,19 +225,18 @@ __global__ void __launch_bounds__(32 * WARPS, 2) walk_kernel(const __grid_consta
           pg.page(a, sg, blk, page, take.j + e, c4_bytes);
         }
         __syncwarp();  // all lanes are done with the stage
-        if (n_put < n_units) issue();
+        if (put.x < limit) issue();
         st = st + 1 == NS ? 0 : st + 1;
       }
 
       // a whole segment, and nothing in front of it: the rows are done
       if (ok) pg.finish(a, sg, out, !p.front && a.n_shared == 0 && take.j == 0 && last == take.P);
       // the next segment
-      if (ok && k < n_units) {
-        take.j = take.P - 1;
-        const int b = take.b;
-        advance(take);
-        seg += 1 + static_cast<int64_t>(take.b - (b == take.b ? b : b + 1)) * a.H * p.groups;  // sequences without pages
-      }
+      take.j += last - 1;
+      take.x += last - 1;
+      const int b = take.b;
+      advance(take);
+      seg += 1 + static_cast<int64_t>(take.b - (b == take.b ? b : b + 1)) * hg;  // sequences without pages
     }
     if (!ok) {  // copies still in flight land before the block's shared memory is released
       report_status(a.status, BITLINEAR_STATUS_TIMEOUT);
@@ -309,10 +321,10 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinA
   };
   if (p.own != nullptr) {
     const int b = tok / a.Sq, r = (tok % a.Sq) * G + gg, grp = r / p.own_cols;
-    const int64_t c = p.cum[b], P = p.cum[b + 1] - c, hg = static_cast<int64_t>(a.H) * p.own_groups;
-    if (P > 0) {
-      const int64_t U = p.cum[a.B] * hg, u = c * hg + (static_cast<int64_t>(h) * p.own_groups + grp) * P;
-      const int64_t nw = walkers(U, p.own_nw), w0 = warp_of(U, u, nw), w1 = warp_of(U, u + P - 1, nw);
+    const int64_t c = p.cum[b], len = p.cum[b + 1] - c, hg = static_cast<int64_t>(a.H) * p.own_groups;
+    if (len > 0) {
+      const int64_t U = p.cum[a.B] * hg, u = c * hg + (static_cast<int64_t>(h) * p.own_groups + grp) * len;
+      const int64_t nw = walkers(U, p.own_nw), w0 = warp_of(U, u + segment_overhead(p.own_cols), nw), w1 = warp_of(U, u + len - 1, nw);
       if (p.front == nullptr && w0 == w1) return;  // the walk has written the row
       add(p.own, p.own_cols, r % p.own_cols, static_cast<int64_t>(b) * hg + static_cast<int64_t>(h) * p.own_groups + grp + w0, w1 - w0 + 1);
     }
@@ -325,8 +337,9 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ JoinA
     else add(p.front, 128, r & 127, 2 * (item + p.tiles.pairs * 2 * k), 2 * k);
   } else if (p.front != nullptr) {
     const int r = tok * G + gg, grp = r / p.front_cols;
-    const int64_t seg = static_cast<int64_t>(h) * p.front_groups + grp, U = static_cast<int64_t>(a.n_shared) * a.H * p.front_groups;
-    const int64_t nw = walkers(U, p.front_nw), w0 = warp_of(U, seg * a.n_shared, nw), w1 = warp_of(U, (seg + 1) * a.n_shared - 1, nw);
+    const int64_t ov = segment_overhead(p.front_cols), len = a.n_shared + ov;
+    const int64_t seg = static_cast<int64_t>(h) * p.front_groups + grp, U = len * a.H * p.front_groups;
+    const int64_t nw = walkers(U, p.front_nw), w0 = warp_of(U, seg * len + ov, nw), w1 = warp_of(U, (seg + 1) * len - 1, nw);
     add(p.front, p.front_cols, r % p.front_cols, seg + w0, w1 - w0 + 1);
   }
   if (p.own == nullptr && p.front == nullptr && lane == 0 && __ldg(a.lens + tok / a.Sq) != 0)
@@ -382,7 +395,7 @@ static Plan::Walk plan_walk(int64_t D, int64_t rows, int64_t segs_per_group, int
   w.cols = rows <= 2 ? 2 : rows <= 4 ? 4 : 8;
   w.groups = static_cast<int>((rows + w.cols - 1) / w.cols);
   if (!any) return w;
-  const int64_t units = max_units_per_group * w.groups;
+  const int64_t units = (max_units_per_group + segs_per_group * segment_overhead(w.cols)) * w.groups;
   const int64_t most = static_cast<int64_t>(per_sm) * num_sms();
   w.grid = static_cast<int>(units < most ? units : most);
   w.nw = static_cast<int64_t>(w.grid) * walk_warps(static_cast<int>(D));
