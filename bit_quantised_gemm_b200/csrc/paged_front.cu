@@ -12,17 +12,21 @@
 //   unpackers   K -> [64 tokens][D], V -> [D][64 tokens] as fp16 codes - 4,
 //               128-byte swizzled; a token kept at 4 bits is one of these rows
 //   scaler      one warp, the scales beside them, and which tokens take part
-//   issuer      one thread: S = Q K^T, O += P V (P in tensor memory where S
-//               was; two S a stream, so that the next one is there when a
-//               softmax ends)
+//   issuers     a warp a stream, of which one thread issues: S = Q K^T (Q in
+//               tensor memory), O += P V (P in tensor memory, where S was).
+//               One for both streams had each wait
+//               for the other's softmax, and its products queue up, which slows
+//               the softmax warp that shares its scheduler
 //   softmax     4 warps a stream, a row a thread: s = S x (K scale), p = 2^(s - r), weights p x (V scale) rounded to fp16
 //               (2^-11 of a weight, a quarter of what the output's rounding
 //               may take). r is the largest s so far plus the largest V scale's
 //               exponent; it moves, and O is multiplied, only when it grows by 8.
-// While one stream's rows are in the softmax, the other's products run.
+// P through shared memory instead (a stream's next scores are then there when
+// its softmax ends) was slower: 105 us against 101 at 96 x 32 heads behind
+// 32768 tokens; the products' operands, the unpackers and the scales already
+// take more than half of what shared memory can move.
+// While one stream is in the softmax, the other's products run.
 //
-// Q is in tensor memory where there is room for it beside two S a stream (D =
-// 64 and 256), in shared memory else.
 #include "launch.h"
 #include "paged.cuh"
 #include "paged_mma.cuh"
@@ -36,16 +40,14 @@ namespace {
 template <int D>
 struct Shape {
   static constexpr int STREAMS = front_streams(D);
-  static constexpr int SBUF = D == 128 ? 1 : 2;      // S buffers of a stream
-  static constexpr bool QS = false;                  // Q in shared memory
   static constexpr int NST = D == 256 ? 2 : 4;       // K and V tiles
   static constexpr int NRAW = D == 256 ? 3 : 4;      // blocks as they come
   static constexpr int SOFT = 4 * STREAMS, UNPACK = D == 256 ? 8 : 4;  // warps
-  static constexpr int LOADER = SOFT + UNPACK, SCALER = LOADER + 1, ISSUER = SCALER + 1, THREADS = 32 * (ISSUER + 1);
+  static constexpr int LOADER = SOFT + UNPACK, SCALER = LOADER + 1, ISSUER = SCALER + 1, THREADS = 32 * (ISSUER + STREAMS);
   static constexpr int RB = row_bytes(D);
-  static constexpr int TILE = PT * D * 2, Q_TILE = QS ? 128 * D * 2 : 0;
-  static constexpr int O = 0, Q = STREAMS * D, S = Q + (QS ? 0 : STREAMS * (D / 2));  // tensor memory columns
-  static_assert(S + STREAMS * SBUF * PT <= 512);
+  static constexpr int TILE = PT * D * 2;
+  static constexpr int O = 0, Q = STREAMS * D, S = Q + STREAMS * (D / 2);  // tensor memory columns
+  static_assert(S + STREAMS * PT <= 512);
 };
 
 template <int D>
@@ -56,7 +58,7 @@ struct Shared {
   int v_exp[H::NST];      // biased exponent of the largest V scale
   int page[H::NRAW];
   uint64_t raw_full[H::NRAW], raw_empty[H::NRAW], k_full[H::NST], v_full[H::NST], v_empty[H::NST];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], pv_done[2], drain;
+  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain[2];
   uint32_t tmem;
   int abort;
 };
@@ -129,14 +131,13 @@ __constant__ uint8_t kPairs[16][4] = {  // pair32's codes and their bits in the 
 template <int D>
 __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __grid_constant__ FrontArgs p) {
   using H = Shape<D>;
-  constexpr int STREAMS = H::STREAMS, SBUF = H::SBUF, NST = H::NST, NRAW = H::NRAW, RB = H::RB;
+  constexpr int STREAMS = H::STREAMS, NST = H::NST, NRAW = H::NRAW, RB = H::RB;
   extern __shared__ __align__(1024) uint8_t dyn[];
   __shared__ Shared<D> sm;
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   uint8_t* base = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
-  uint8_t* q_tile = base;
-  uint8_t* k_tile = base + STREAMS * H::Q_TILE;
+  uint8_t* k_tile = base;
   uint8_t* v_tile = k_tile + NST * H::TILE;
   uint8_t* raw = v_tile + NST * H::TILE;
 
@@ -165,16 +166,17 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     for (int i = 0; i < NRAW; ++i) { mbar_init(&sm.raw_full[i], 1); mbar_init(&sm.raw_empty[i], H::UNPACK + 1); }
     for (int i = 0; i < NST; ++i) {
       mbar_init(&sm.k_full[i], H::UNPACK + 1);
-      mbar_init(&sm.v_full[i], H::UNPACK); mbar_init(&sm.v_empty[i], 1);
+      mbar_init(&sm.v_full[i], H::UNPACK); mbar_init(&sm.v_empty[i], pair ? 2 : 1);
     }
     for (int t = 0; t < STREAMS; ++t) {
       const int live = (stream_rows(t) + 31) / 32;  // warps with rows
       mbar_init(&sm.q_full[t], live);
-      for (int b = 0; b < SBUF; ++b) { mbar_init(&sm.s_full[t][b], 1); mbar_init(&sm.p_full[t][b], live); }
+      mbar_init(&sm.s_full[t], 1);
+      mbar_init(&sm.p_full[t], live);
       mbar_init(&sm.pv_done[t], 1);
+      mbar_init(&sm.drain[t], 1);
     }
-    mbar_init(&sm.drain, 1);
-    sm.abort = 0;
+      sm.abort = 0;
     fence_mbar_init();
   }
   if (warp == H::ISSUER) { tmem_alloc(&sm.tmem, 512); tmem_relinquish(); }
@@ -217,57 +219,45 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     }
     if (*abort)  // copies in flight land before the memory is released
       for (int i = max(0, put - NRAW); i < put; ++i) mbar_wait(&sm.raw_full[i % NRAW], (i / NRAW) & 1, a.timeout_ns, nullptr);
-  } else if (warp == H::ISSUER) {
+  } else if (warp >= H::ISSUER) {
     // the warp stays together in the waits; one lane issues
     constexpr uint32_t idS = make_idesc(1, 0, 0, 128, PT), idO = make_idesc(1, 0, 0, 128, D);
-    const uint32_t q_lo = desc_lo(smem_u32(q_tile)), k_lo = desc_lo(smem_u32(k_tile)), v_lo = desc_lo(smem_u32(v_tile));
+    const int t = warp - H::ISSUER, np = stream_pages(t);
+    const uint32_t k_lo = desc_lo(smem_u32(k_tile)), v_lo = desc_lo(smem_u32(v_tile));
     const bool lead = elect_one() != 0;
-    int n_s[2] = {0, 0};
-    bool ok = true;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xFFFFFFFFu, wait(bar, parity)) != 0; };
-    auto issue_s = [&](int t) {
-      const int k = n_s[t]++, pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
-      if ((alternate || t == 0) && !(ok = wait_all(&sm.k_full[st], pg / NST))) return;
-      tc_fence_after();
-      if (lead) {
-        const uint32_t kt = k_lo + st * (H::TILE >> 4), d = tm + H::S + (t * SBUF + b) * PT, qt = q_lo + t * (H::Q_TILE >> 4);
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint64_t bd = desc_at(kt, (i >> 2) * (PT * 8) + (i & 3) * 2);
-          if constexpr (H::QS) mma_f16_ss(d, desc_at(qt, (i >> 2) * (128 * 8) + (i & 3) * 2), bd, idS, i > 0);
-          else mma_f16_ts(d, tm + H::Q + t * (D / 2) + 8 * i, bd, idS, i > 0);
-        }
-        tc_commit(&sm.s_full[t][b]);
-      }
-      __syncwarp();
-    };
-    for (int t = 0; t < STREAMS && ok; ++t)
-      if (stream_pages(t) > 0) ok = wait_all(&sm.q_full[t], 0);
-    tc_fence_after();
-    for (int b = 0; b < SBUF; ++b)
-      for (int t = 0; t < STREAMS; ++t)
-        if (ok && b < stream_pages(t)) issue_s(t);
-    for (int k = 0; k < stream_pages(0) && ok; ++k)
-      for (int t = 0; t < STREAMS; ++t) {
-        if (!ok || k >= stream_pages(t)) continue;
-        const int pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
-        if (alternate || t == 0) ok = wait_all(&sm.v_full[st], pg / NST);
-        if (!(ok = ok && wait_all(&sm.p_full[t][b], k / SBUF))) break;
+    bool ok = np == 0 || wait_all(&sm.q_full[t], 0);
+    for (int k = 0; k <= np && ok; ++k) {
+      if (k > 0) {  // values of the page before
+        const int pg = alternate ? 2 * (k - 1) + t : k - 1, st = pg % NST;
+        if (!(ok = wait_all(&sm.v_full[st], pg / NST) && wait_all(&sm.p_full[t], k - 1))) break;
         tc_fence_after();
         if (lead) {
           const uint32_t vt = v_lo + st * (H::TILE >> 4);
 #pragma unroll
-          for (int i = 0; i < PT / 16; ++i)
-            mma_f16_ts(tm + H::O + t * D, tm + H::S + (t * SBUF + b) * PT + 8 * i, desc_at(vt, 2 * i), idO, k > 0 || i > 0);
+          for (int i = 0; i < PT / 16; ++i) mma_f16_ts(tm + H::O + t * D, tm + H::S + t * PT + 8 * i, desc_at(vt, 2 * i), idO, k > 1 || i > 0);
           tc_commit(&sm.pv_done[t]);
-          if (alternate || t == STREAMS - 1) tc_commit(&sm.v_empty[st]);
+          tc_commit(&sm.v_empty[st]);
         }
         __syncwarp();
-        if (n_s[t] < stream_pages(t)) issue_s(t);
       }
+      if (k < np) {  // scores of page k (in issue order behind the products that read P in their place)
+        const int pg = alternate ? 2 * k + t : k, st = pg % NST;
+        if (!(ok = wait_all(&sm.k_full[st], pg / NST))) break;
+        tc_fence_after();
+        if (lead) {
+          const uint32_t kt = k_lo + st * (H::TILE >> 4);
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)
+            mma_f16_ts(tm + H::S + t * PT, tm + H::Q + t * (D / 2) + 8 * i, desc_at(kt, (i >> 2) * (PT * 8) + (i & 3) * 2), idS, i > 0);
+          tc_commit(&sm.s_full[t]);
+        }
+        __syncwarp();
+      }
+    }
     if (!ok && lead) {  // what was issued ends before the memory is released
-      tc_commit(&sm.drain);
-      mbar_wait(&sm.drain, 0, a.timeout_ns, nullptr);
+      tc_commit(&sm.drain[t]);
+      mbar_wait(&sm.drain[t], 0, a.timeout_ns, nullptr);
     }
     __syncwarp();
   } else if (warp == H::SCALER) {
@@ -474,16 +464,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
             const Pair pr = pair32(i);
             y[i] = pack_f16x2(qf(pr.lo) * (1.f / (1 << (3 * pr.lo - pr.n))), qf(pr.hi) * (1.f / (1 << (3 * pr.hi - pr.n - 16))));
           }
-          if constexpr (H::QS) {
-            const uint32_t dst = smem_u32(q_tile + t * H::Q_TILE) + (c >> 1) * (128 * 128) + col * 128;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st_shared_v4(dst + ((((c & 1) * 4 + i) ^ (col & 7)) << 4), y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-          } else {
-            tmem_st16(tm + lanes + H::Q + t * (D / 2) + 16 * c, y);
-          }
+          tmem_st16(tm + lanes + H::Q + t * (D / 2) + 16 * c, y);
         }
-        if constexpr (H::QS) fence_proxy_async_smem();
-        else { tmem_st_wait(); tc_fence_before(); }
+        tmem_st_wait();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_full[t]);
       }
@@ -493,15 +477,14 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       float ref = -INFINITY, l = 0.f;
       bool ok = true;
       for (int k = opaque_zero(); k < np; ++k) {
-        const int pg = alternate ? 2 * k + t : k, st = pg % NST, b = k % SBUF;
-        const uint32_t s_col = tm + lanes + H::S + (t * SBUF + b) * PT;
-        ok = wait(&sm.s_full[t][b], k / SBUF);  // (the page's scales were there before S was begun)
+        const int pg = alternate ? 2 * k + t : k, st = pg % NST;
+        ok = wait(&sm.s_full[t], k);  // (the page's scales were there before S was begun)
         if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
         tc_fence_after();
         float2 s[PT / 2];
         {
           uint32_t x[PT];
-          tmem_ld64(s_col, x);
+          tmem_ld64(tm + lanes + H::S + t * PT, x);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < PT; i += 4) {
@@ -568,11 +551,11 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
           w[i / 2 + 1] = pack_f16x2(u.y, v.y);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_st32(s_col, w);
+        tmem_st32(tm + lanes + H::S + t * PT, w);
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[t][b]);
+        if (lane == 0) mbar_arrive(&sm.p_full[t]);
       }
       // ---- the piece
       if (ok && np > 0) {
@@ -617,7 +600,7 @@ cudaError_t launch_front_t(const AttnArgs& a, const FrontPlan& plan, float* part
   p.parts = parts;
   p.c4_bytes = a.C4 <= kStageRows4 ? a.C4 * D : 0;
   p.raw_bytes = block_bytes(D) + p.c4_bytes;
-  const int smem = 1024 + H::STREAMS * H::Q_TILE + 2 * H::NST * H::TILE + H::NRAW * p.raw_bytes;
+  const int smem = 1024 + 2 * H::NST * H::TILE + H::NRAW * p.raw_bytes;
   const cudaError_t e = set_smem_limit(front_kernel<D>, smem);
   if (e != cudaSuccess) return e;
   return launch_kernel(front_kernel<D>, dim3(static_cast<unsigned>(plan.items)), dim3(H::THREADS), smem, s, 0u, p);
