@@ -77,6 +77,26 @@ def test_append_aligned_run(D):
         assert np.array_equal(pages.cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("D,H", [(64, 3), (128, 2), (256, 5)])
+@pytest.mark.parametrize("first", [0, 4, 13, 60])
+def test_append_prompt(D, H, first):
+    """A prompt from some place of a page on, with padding behind it, then with one token at 4 bits in its middle:
+    whole runs of tokens, runs cut by page borders, and tokens alone at both ends."""
+    rng = np.random.default_rng(D + first)
+    n = 150
+    k, v = W.normal_bf16(rng, (n, H, D)), W.normal_bf16(rng, (n, H, D))
+    n_pages = (first + n + 63) // 64
+    order = rng.permutation(n_pages)
+    slots = np.array([order[(first + i) // 64] * 64 + (first + i) % 64 for i in range(n)])
+    slots[n - 5:] = -1
+    for row4 in (np.full(n, -1), np.where(np.arange(n) == 70, 1, -1)):
+        want, want4 = np.full((n_pages, H, P.block_bytes(D)), 0x5A, np.uint8), np.full((n_pages, H, 2, D), 0x5A, np.uint8)
+        pages, codes4 = torch.from_numpy(want.copy()).to(DEV), torch.from_numpy(want4.copy()).to(DEV)
+        P.append(want, want4, k, v, slots, row4)
+        B.kv_append_3bit(up(k), up(v), ints(slots), pages, row4=ints(row4), codes4=codes4)
+        assert np.array_equal(pages.cpu().numpy(), want) and np.array_equal(codes4.cpu().numpy(), want4)
+
+
 def test_append_values_at_borders():
     """Zero rows (the scale's floor), tiny and large rows, exact ties of the codes."""
     D, H = 128, 2
@@ -346,6 +366,77 @@ def test_attention_many_rows_on_a_prefix(Bn, G, Sq, D, shared):
     check(q, pages, codes4, tables, lens, rng.permutation(shared))
 
 
+@pytest.mark.parametrize("D,shared,C4", [(64, 7, 0), (64, 2, 5), (128, 9, 0), (128, 1, 1), (128, 5, 6), (256, 3, 0), (256, 6, 4)])
+@pytest.mark.parametrize("Bn", [17, 128, 260, 300])
+def test_attention_tiles_on_a_prefix(D, shared, C4, Bn):
+    """One tile of rows, two, and an odd one beside a pair; odd and even numbers of pages, one page; more 4-bit
+    rows a page than travel with it; sequences that end before, inside and at the end of the prefix."""
+    rng = np.random.default_rng(D + shared + Bn)
+    pages, codes4 = pool(rng, shared + 2, 1, D, C4)
+    lens = 64 * shared + rng.integers(0, 40, Bn)
+    lens[0], lens[5], lens[6], lens[Bn // 2] = 0, 64 * shared - 1, 1, 64 * shared
+    tables = shared + rng.integers(0, 2, (Bn, 1))
+    q = W.normal_bf16(rng, (Bn, 1, 1, D))
+    got = check(q, pages, codes4, tables, lens, rng.permutation(shared))
+    assert (got[0] == 0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_tiles_unwritten_and_bad(D):
+    """What no token has written behind the last one of the prefix counts for nothing, and a page that is none is
+    passed over, 4-bit rows out of range are left out; both are reported."""
+    rng = np.random.default_rng(D)
+    Bn, shared = 40, 4
+    pages, codes4 = pool(rng, 6, 2, D, 1)
+    rb = 3 * D // 8
+    blk = pages[3]
+    for o in range(20, 64):  # page 3, the prefix's last: 20 tokens
+        blk[:, o * rb:(o + 1) * rb] = 0xFF
+        at = 64 * rb + (o // 4) * 4 * rb + o % 4
+        blk[:, at:at + 4 * rb:4] = 0xFF
+        blk[:, 128 * rb + 4 * o:128 * rb + 4 * o + 4] = 0xFF
+        blk[:, 128 * rb + 256 + 4 * o:128 * rb + 256 + 4 * o + 4] = [0, 0, 0x80, 0x7F]
+    q = W.normal_bf16(rng, (Bn, 1, 2, D))
+    lens = rng.integers(1, 64 * 3 + 20, Bn)
+    lens[3] = 64 * 3 + 20
+    none = np.zeros((Bn, 0), np.int64)
+    check(q, pages, codes4, none, lens, [0, 1, 2, 3])
+    # a page that is none: as if its tokens were not there
+    dev = (up(q), torch.from_numpy(pages).to(DEV), ints(none).view(Bn, 0), ints(np.full(Bn, 64 * 3)))
+    c4 = torch.from_numpy(codes4).to(DEV)
+    st = fresh()
+    got = B.kv_attention_3bit_paged(*dev, shared=ints([0, 6, 2]), codes4=c4, status=st)
+    assert st.item() == _lib.STATUS_BAD_INDEX
+    want, A = P.attention(q, pages, codes4, none, np.full(Bn, 128), [0, 2])
+    err = np.abs(O.bf16_to_f32(bits(got)).astype(np.float64) - want)
+    assert (err <= tolerance(want, A)).all()
+    # the 4-bit token of each page without its row: left out
+    st = fresh()
+    got = B.kv_attention_3bit_paged(*dev[:3], ints(np.full(Bn, 64)), shared=ints([1]), status=st)
+    assert st.item() == _lib.STATUS_BAD_INDEX
+    o4 = int(np.flatnonzero(np.signbit(pages[1, 0, 128 * rb:].view(np.float32)[:64]))[0])
+    keep = np.array([o for o in range(64) if o != o4])
+    kv = [P.read(pages, codes4, 1, o, D) for o in keep]
+    k, v = (np.stack([x[i] for x in kv]) for i in range(2))
+    for h in range(2):
+        s = np.einsum("bd,td->bt", O.bf16_to_f32(q[:, 0, h]).astype(np.float64), k[:, h]) / np.sqrt(D)
+        p = np.exp(s - s.max(-1, keepdims=True))
+        p /= p.sum(-1, keepdims=True)
+        want, A = p @ v[:, h], p @ np.abs(v[:, h])
+        err = np.abs(O.bf16_to_f32(bits(got))[:, 0, h].astype(np.float64) - want)
+        assert (err <= tolerance(want, A)).all()
+
+
+def test_attention_more_sequences_than_threads():
+    """Lengths are summed by chunks of sequences, and a warp finds its place between them."""
+    rng = np.random.default_rng(14)
+    D, Bn = 64, 700
+    pages, _ = pool(rng, 6, 1, D, 0)
+    lens = np.where(rng.integers(0, 3, Bn) == 0, 0, rng.integers(0, 130, Bn))
+    q = W.normal_bf16(rng, (Bn, 1, 1, D))
+    check(q, pages, None, rng.integers(0, 6, (Bn, 3)), lens, [])
+
+
 @pytest.mark.parametrize("D,G", [(64, 1), (128, 1), (128, 4), (256, 2)])
 def test_attention_long(D, G):
     """Long enough that one sequence's pages go to many warps, two lengths far apart."""
@@ -524,6 +615,40 @@ def test_run_on_a_stream_of_its_own():
     with torch.cuda.stream(s):
         decode_run(2, 128, 1, 3, stream=s)
     s.synchronize()
+
+
+def test_two_graphs_and_a_workspace():
+    """Two captured calls that use one workspace, replayed in turn, after the tables, lengths and queries have changed."""
+    rng = np.random.default_rng(15)
+    D, H = 128, 2
+    pages, codes4 = pool(rng, 12, H, D, 1)
+    p, c4 = torch.from_numpy(pages).to(DEV), torch.from_numpy(codes4).to(DEV)
+    Bn, shared = 20, 3
+    sets = []
+    for i in range(2):
+        q = up(W.normal_bf16(rng, (Bn, 1, H, D)))
+        sets.append(dict(q=q, tables=ints(rng.integers(0, 12, (Bn, 2))), lens=ints(64 * shared + rng.integers(1, 120, Bn)),
+                         shared=ints(rng.permutation(12)[:shared])))
+    work = B.kv_attention_3bit_paged_workspace(sets[0]["q"], p, sets[0]["tables"], sets[0]["shared"])
+
+    def call(s, **kw):
+        return B.kv_attention_3bit_paged(s["q"], p, s["tables"], s["lens"], shared=s["shared"], codes4=c4, **kw)
+
+    call(sets[0], workspace=work)
+    graphs = []
+    for s in sets:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = call(s, workspace=work)
+        graphs.append((g, out))
+    for _ in range(3):
+        for s in sets:
+            s["q"].copy_(up(W.normal_bf16(rng, (Bn, 1, H, D))))
+            s["lens"].copy_(ints(rng.integers(0, 64 * shared + 128, Bn)))
+            s["tables"].copy_(ints(rng.integers(0, 12, (Bn, 2))))
+        for (g, out), s in zip(graphs, sets):
+            g.replay()
+            assert torch.equal(out, call(s))
 
 
 def test_two_calls_at_once():
