@@ -195,4 +195,21 @@ inline cudaError_t launch_kernel(void (*kern)(Exp...), dim3 grid, dim3 block, si
   return cudaLaunchKernelEx(&cfg, kern, static_cast<Act&&>(args)...);
 }
 
+// As launch_kernel, for a later kernel of one call: it may always start before
+// the kernel ahead of it has ended, and waits for that one itself (pdl_wait).
+template <typename K, typename... A>
+inline cudaError_t launch_behind(K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 }  // namespace blt

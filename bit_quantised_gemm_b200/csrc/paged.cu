@@ -281,7 +281,7 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
 // walk over refs with a running count. The walk writes them into the tables
 // behind the rows' ends, where entries say nothing yet; only when all needs
 // are met do references, lengths and left pages change.
-constexpr int kWalk = 16;  // reference counts a thread takes at a time
+constexpr int kWalk = 16;  // reference counts that a thread takes at a time, at most
 
 __global__ void __launch_bounds__(kBig) grow_kernel(const TableArgs t, const int32_t* __restrict__ rows,
                                                     const int32_t* __restrict__ n_new, int n, int max_new,
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kBig) grow_kernel(const TableArgs t, const int
                                                     int32_t* __restrict__ cow_dst) {
   pdl_wait();
   pdl_trigger();
-  __shared__ int s_row[kBig], s_len[kBig], s_new[kBig], s_last[kBig], s_first[kBig + 1], s_page[kBig];
+  __shared__ int s_row[kBig], s_len[kBig], s_new[kBig], s_last[kBig], s_first[kBig + 1], s_page[kBig], s_count[kBig];
   __shared__ int s_warp[32];
   const int i = threadIdx.x;
   int row = -1, len = 0, add = 0, last = -1;
@@ -303,10 +303,19 @@ __global__ void __launch_bounds__(kBig) grow_kernel(const TableArgs t, const int
       bad = len < 0 || (static_cast<int64_t>(len) + add + PT - 1) / PT > t.W;
     }
   }
+  // an entry's earlier ones of the same row, and of the same last page below: all pairs over all threads
+  auto earlier = [&](const int* of) {
+    s_count[i] = 0;
+    __syncthreads();
+    for (int k = i; k < n * n; k += kBig) {
+      const int e = k / n, j = k - e * n;
+      if (j < e && of[j] == of[e]) atomicAdd(&s_count[e], 1);
+    }
+    __syncthreads();
+    return s_count[i];
+  };
   s_row[i] = row;
-  __syncthreads();
-  if (i < n && !bad)
-    for (int j = 0; j < i; ++j) bad |= s_row[j] == row;
+  bad |= earlier(s_row) > 0;
   const int have = pages_of(len);
   if (i < n && !bad && add > 0 && len % PT != 0) {
     last = t.tables[static_cast<int64_t>(row) * t.ldt + have - 1];
@@ -314,16 +323,9 @@ __global__ void __launch_bounds__(kBig) grow_kernel(const TableArgs t, const int
   }
   if (bad) { add = 0; report_status(t.status, BITLINEAR_STATUS_BAD_INDEX); }
   s_last[i] = last;
-  __syncthreads();
-  bool copy = false;
-  if (last >= 0) {
-    const int r = t.refs[last];
-    if (r > 1) {
-      int before = 0;
-      for (int j = 0; j < i; ++j) before += s_last[j] == last;
-      copy = r - before > 1;
-    }
-  }
+  const int shares = last >= 0 ? t.refs[last] : 0;
+  const int before = earlier(s_last);
+  const bool copy = shares > 1 && shares - before > 1;
   const int need = i < n && !bad ? pages_of(len + add) - have + (copy ? 1 : 0) : 0;
   int total;
   const int upto = block_scan(need, s_warp, &total);
@@ -335,13 +337,15 @@ __global__ void __launch_bounds__(kBig) grow_kernel(const TableArgs t, const int
   __syncthreads();
 
   // the lowest `total` free pages
+  // (a small pool over all threads: a thread that finds several pages places them one after the other)
   int found = 0;
-  for (int64_t base = 0; base < t.n_pages && found < total; base += kBig * kWalk) {
-    const int64_t at = base + static_cast<int64_t>(i) * kWalk;
+  const int walk = min(kWalk, (t.n_pages + kBig - 1) / kBig);
+  for (int64_t base = 0; base < t.n_pages && found < total; base += kBig * walk) {
+    const int64_t at = base + static_cast<int64_t>(i) * walk;
     uint32_t zero = 0u;
 #pragma unroll
     for (int k = 0; k < kWalk; ++k)
-      if (at + k < t.n_pages && t.refs[at + k] == 0) zero |= 1u << k;
+      if (k < walk && at + k < t.n_pages && t.refs[at + k] == 0) zero |= 1u << k;
     int sum;
     int j = found + block_scan(__popc(zero), s_warp, &sum) - __popc(zero);
     while (zero && j < total) {
@@ -474,12 +478,16 @@ cudaError_t launch_paged_append(const paged::AppendArgs& a, int64_t D, cudaStrea
   return go(paged::append_kernel<8>);
 }
 
-cudaError_t launch_pages_copy(const paged::CopyArgs& a, cudaStream_t s) {
+static cudaError_t pages_copy(const paged::CopyArgs& a, cudaStream_t s, bool behind) {
   const int64_t pieces = (a.page_bytes + paged::kCopyPiece - 1) / paged::kCopyPiece +
                          (a.page_bytes4 + paged::kCopyPiece - 1) / paged::kCopyPiece;
   const int64_t want = a.n * a.L * pieces, cap = 8LL * num_sms();
-  return launch_kernel(paged::copy_kernel, dim3(static_cast<unsigned>(want < cap ? want : cap)), dim3(256), 0, s, 0u, a);
+  const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
+  return behind ? launch_behind(paged::copy_kernel, grid, dim3(256), 0, s, a)
+                : launch_kernel(paged::copy_kernel, grid, dim3(256), 0, s, 0u, a);
 }
+
+cudaError_t launch_pages_copy(const paged::CopyArgs& a, cudaStream_t s) { return pages_copy(a, s, false); }
 
 cudaError_t launch_pages_fork(const paged::TableArgs& t, const int32_t* parents, const int32_t* children, int64_t n,
                               cudaStream_t s) {
@@ -504,7 +512,7 @@ cudaError_t launch_pages_grow(const paged::TableArgs& t, const int32_t* rows, co
   a.dst = cow + n;
   a.n = n;
   a.count = nullptr;
-  return launch_pages_copy(a, s);
+  return pages_copy(a, s, true);
 }
 
 cudaError_t launch_pages_compact(const paged::TableArgs& t, const paged::CopyArgs& c, int32_t* work,
@@ -521,9 +529,9 @@ cudaError_t launch_pages_compact(const paged::TableArgs& t, const paged::CopyArg
   a.dst = dst;
   a.n = (t.n_pages + 1) / 2;
   a.count = count;
-  e = launch_pages_copy(a, s);
+  e = pages_copy(a, s, true);
   if (e != cudaSuccess || t.R == 0) return e;
-  return launch_kernel(paged::compact_tables_kernel, dim3(static_cast<unsigned>(t.R)), dim3(128), 0, s, 0u, t,
+  return launch_behind(paged::compact_tables_kernel, dim3(static_cast<unsigned>(t.R)), dim3(128), 0, s, t,
                        static_cast<const int32_t*>(map), static_cast<const int32_t*>(n_live));
 }
 

@@ -442,22 +442,6 @@ static Plan make_plan(int64_t B, int64_t Sq, int64_t Hq, int64_t H, int64_t D, i
   return p;
 }
 
-// As launch_kernel, and may always start before the kernel ahead of it has ended.
-template <typename K, typename... A>
-static cudaError_t launch_behind(K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = grid;
-  cfg.blockDim = block;
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <int D, typename Page>
 static cudaError_t launch_walk(const AttnArgs& a, const Plan::Walk& w, bool front, bool behind, float* parts, int64_t* cum,
                                cudaStream_t s) {
