@@ -427,6 +427,38 @@ def test_attention_tiles_unwritten_and_bad(D):
         assert (err <= tolerance(want, A)).all()
 
 
+@pytest.mark.parametrize("G", [1, 4, 8])
+def test_attention_one_page_many_times(G):
+    """A table that names one page 1.25 million times, more than 500 times for each warp: the answer is the page's own."""
+    rng = np.random.default_rng(G)
+    D, W_ = 64, 148 * 2 * 8 * 530
+    pages, _ = pool(rng, 1, 1, D, 0)
+    q = W.normal_bf16(rng, (1, 1, G, D))
+    st = fresh()
+    got = B.kv_attention_3bit_paged(up(q), torch.from_numpy(pages).to(DEV), torch.zeros(1, W_, dtype=torch.int32, device=DEV),
+                                    ints([64 * W_]), status=st)
+    o, A = P.attention(q, pages, None, np.zeros((1, 1), int), [64])
+    # 530 pages of 4 steps, each rounding a sum of up to 7/4 of 4/3 A by 2^-23: 2120 * 7/3 * 2^-23 < 2^-10
+    bound = tolerance(o, A) + 2.0 ** -10 * A.max(-1, keepdims=True)
+    assert st.item() == 0 and (np.abs(O.bf16_to_f32(bits(got)) - o) <= bound).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_one_shared_page_many_times(D):
+    """The same for the tiles: a prefix that is one page 20000 times."""
+    rng = np.random.default_rng(D)
+    pages, _ = pool(rng, 1, 2, D, 0)
+    n, Bn = 20000, 40
+    q = W.normal_bf16(rng, (Bn, 1, 2, D))
+    st = fresh()
+    got = B.kv_attention_3bit_paged(up(q), torch.from_numpy(pages).to(DEV), torch.zeros(Bn, 0, dtype=torch.int32, device=DEV),
+                                    ints(np.full(Bn, 64 * n)), shared=ints(np.zeros(n)), status=st)
+    o, A = P.attention(q, pages, None, np.zeros((Bn, 1), int), np.full(Bn, 64))
+    # up to 20000 / 18 pages a stream, 4 steps each, as above
+    bound = tolerance(o, A) + 2.0 ** -9 * A.max(-1, keepdims=True)
+    assert st.item() == 0 and (np.abs(O.bf16_to_f32(bits(got)) - o) <= bound).all()
+
+
 def test_attention_more_sequences_than_threads():
     """Lengths are summed by chunks of sequences, and a warp finds its place between them."""
     rng = np.random.default_rng(14)
@@ -617,6 +649,35 @@ def test_run_on_a_stream_of_its_own():
     s.synchronize()
 
 
+def tile_calls(n):
+    rng = np.random.default_rng(12)
+    pages, _ = pool(rng, 40, 4, 128, 0)
+    p = torch.from_numpy(pages).to(DEV)
+    calls = []
+    for i in range(n):
+        q = up(W.normal_bf16(rng, (24, 1, 8, 128)))
+        lens = ints(64 * 8 + rng.integers(1, 100, 24))
+        calls.append((q, p, ints(rng.integers(0, 40, (24, 2))), lens, ints(rng.permutation(40)[:8])))
+    return calls
+
+
+def test_run_overlapped():
+    """Every kernel may start before the one ahead of it in the stream has ended."""
+    B.set_launch_overlap(True)
+    try:
+        decode_run(2, 128, 2, 4)
+        decode_run(1, 64, 1, 3, seed=12)
+        calls = tile_calls(3)
+        want = [B.kv_attention_3bit_paged(*c[:4], shared=c[4]) for c in calls]
+        torch.cuda.synchronize()
+        for _ in range(10):
+            got = [B.kv_attention_3bit_paged(*c[:4], shared=c[4]) for c in calls]
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+    finally:
+        B.set_launch_overlap(False)
+
+
 def test_two_graphs_and_a_workspace():
     """Two captured calls that use one workspace, replayed in turn, after the tables, lengths and queries have changed."""
     rng = np.random.default_rng(15)
@@ -653,14 +714,7 @@ def test_two_graphs_and_a_workspace():
 
 def test_two_calls_at_once():
     """Two streams, a workspace each, the same pool: what one call after the other gives."""
-    rng = np.random.default_rng(12)
-    pages, _ = pool(rng, 40, 4, 128, 0)
-    p = torch.from_numpy(pages).to(DEV)
-    calls = []
-    for i in range(2):
-        q = up(W.normal_bf16(rng, (24, 1, 8, 128)))
-        lens = ints(64 * 8 + rng.integers(1, 100, 24))
-        calls.append((q, p, ints(rng.integers(0, 40, (24, 2))), lens, ints(rng.permutation(40)[:8])))
+    calls = tile_calls(2)
     want = [B.kv_attention_3bit_paged(*c[:4], shared=c[4]) for c in calls]
     streams = [torch.cuda.Stream() for _ in calls]
     torch.cuda.synchronize()
