@@ -9,7 +9,8 @@
 //   * the sequences' own pages: the Sq Hq / H rows of a sequence that read
 //     one cache head are the columns of its pages' products;
 //   * the shared pages: the rows of ALL sequences are their columns, so a
-//     shared page is read once for the batch (once for every 8 rows);
+//     shared page is read once for the batch (once for every 8 rows; from 17
+//     rows on paged_front.cu has them, 128 a tile);
 //   * a walk leaves, for each stretch of pages that a warp took of one (head,
 //     group of columns), the running maximum, sum and value sums ("a piece");
 //     the join adds a row's pieces of both walks.
@@ -26,8 +27,8 @@ namespace paged {
 
 // --------------------------------------------------------------------- walk
 // The pages of one (sequence, head, group of columns) are a segment. Segments
-// lie one behind the other, each as long as its pages and kOverhead more (what
-// beginning and ending one costs, in pages: without it a warp among one-page
+// lie one behind the other, each as long as its pages and segment_overhead()
+// more (what beginning and ending one costs, in pages: without it a warp among one-page
 // sequences took 27 segments where others took one), and warp w of NW takes
 // the pages that lie in [U w / NW, U (w + 1) / NW): equal shares whatever the
 // lengths are. Each warp streams its pages' blocks (one bulk copy a block)
@@ -45,7 +46,6 @@ struct WalkArgs {
   float* parts;     // pieces
   int64_t* cum;     // [B + 1] length of one head's and group's segments before sequence b (written)
 };
-
 
 // warps with a share of a line of U (each one unit at least), where that of warp w begins, and the warp that has unit u
 __device__ __forceinline__ int64_t walkers(int64_t U, int64_t NW) { return U < NW ? U : NW; }

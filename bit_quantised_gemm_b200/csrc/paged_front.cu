@@ -14,19 +14,23 @@
 //   scaler      one warp, the scales beside them, and which tokens take part
 //   issuers     a warp a stream, of which one thread issues: S = Q K^T (Q in
 //               tensor memory), O += P V (P in tensor memory, where S was).
-//               One for both streams had each wait
-//               for the other's softmax, and its products queue up, which slows
-//               the softmax warp that shares its scheduler
-//   softmax     4 warps a stream, a row a thread: s = S x (K scale), p = 2^(s - r), weights p x (V scale) rounded to fp16
-//               (2^-11 of a weight, a quarter of what the output's rounding
-//               may take). r is the largest s so far plus the largest V scale's
-//               exponent; it moves, and O is multiplied, only when it grows by 8.
-// P through shared memory instead (a stream's next scores are then there when
-// its softmax ends) was slower: 105 us against 101 at 96 x 32 heads behind
-// 32768 tokens; the products' operands, the unpackers and the scales already
-// take more than half of what shared memory can move.
+//               One warp for both streams had each wait for the other's softmax,
+//               and its products queue up, which slows the softmax warps that
+//               share its scheduler
+//   softmax     4 warps a stream, a row a thread: s = S x (K scale),
+//               p = 2^(s - r), weights p x (V scale) rounded to fp16 (2^-11 of a
+//               weight, a quarter of what the output's rounding may take). r is
+//               the largest s so far plus the largest V scale's exponent; it
+//               moves, and O is multiplied, only when it grows by 8
 // While one stream is in the softmax, the other's products run.
 //
+// A page of two tiles takes 3500 clocks at D = 128, where the tensor pipe and
+// the exponentials need 1024 each: a stream's chain of products, barriers,
+// tensor-memory load, maximum and weights is 3500 long, and tensor memory holds
+// no third stream and no second S. P through shared memory (the next S is then
+// there when a softmax ends) was slower, 105 us against 101 at 96 x 32 heads
+// behind 32768 tokens: the products' operands, the unpackers and the scales
+// already take more than half of what shared memory can move.
 #include "launch.h"
 #include "paged.cuh"
 #include "paged_mma.cuh"
@@ -91,13 +95,6 @@ __device__ __forceinline__ uint64_t desc_at(uint32_t lo, uint32_t words) {
   return d;
 }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | 1u << 16; }
-
-// 0, but the compiler does not know: what follows from it stays out of the uniform registers and their pipe
-__device__ __forceinline__ int opaque_zero() {
-  int z;
-  asm volatile("mov.u32 %0, 0;" : "=r"(z));
-  return z;
-}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -168,7 +165,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       mbar_init(&sm.pv_done[t], 1);
       mbar_init(&sm.drain[t], 1);
     }
-      sm.abort = 0;
+    sm.abort = 0;
     fence_mbar_init();
   }
   if (warp == H::ISSUER) { tmem_alloc(&sm.tmem, 512); tmem_relinquish(); }
@@ -295,7 +292,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     const int ut = tid - 32 * H::SOFT, uw = warp - H::SOFT;
     // K: a lane a token's chunk of 32 codes; 8 (16) tokens x 4 (2) chunks a warp and step: no bank conflicts
     constexpr int CH = D / 32, CW = CH < 4 ? CH : 4, TW = 32 / CW, STEPS = PT * CH / (32 * H::UNPACK);
-    const int e = lane & 7, dg = ut >> 3;  // V: a lane 8 dimensions of 8 tokens
+    const int e = lane & 7, dg = ut >> 3;  // V: a lane 8 dimensions of the tokens 4 e .. and 32 + 4 e ..
     const int p_lo = kPairs[lane & 15][0], p_hi = kPairs[lane & 15][1], p_jl = kPairs[lane & 15][2], p_jh = kPairs[lane & 15][3];
     // the words of a page, taken while the page before it is worked on
     uint32_t kw[STEPS][3], vw[2][3];
@@ -316,7 +313,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       if (ut < D) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          const uint32_t* w = reinterpret_cast<const uint32_t*>(src + off_v(D) + (2 * e + q) * 4 * RB + 12 * dg);
+          const uint32_t* w = reinterpret_cast<const uint32_t*>(src + off_v(D) + (e + 8 * q) * 4 * RB + 12 * dg);
 #pragma unroll
           for (int i = 0; i < 3; ++i) vw[q][i] = w[i];
         }
@@ -395,12 +392,12 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         const uint32_t dst = vt + dg * 1024;
 #pragma unroll
         for (int d = 0; d < 8; ++d) st_shared_v4(dst + d * 128 + ((e ^ d) << 4), x[d][0], x[d][1], x[d][2], x[d][3]);
-        for (uint64_t m = four; m; m &= m - 1) {  // 4-bit tokens: token i of the 8 is word 2 (i / 4) + i % 2, half i / 2 % 2
+        for (uint64_t m = four; m; m &= m - 1) {  // 4-bit tokens: word 2 (o / 32) + o % 2, half o / 2 % 2
           const int o = __ffsll(static_cast<long long>(m)) - 1, j = src[o * RB];
-          if ((o >> 3) != e) continue;
+          if (((o >> 2) & 7) != e) continue;
           const uint8_t* r4 = p.c4_bytes ? src + block_bytes(D) + j * D : a.codes4 + ((static_cast<int64_t>(now) * a.H + h) * a.C4 + j) * D;
           const uint32_t y = *reinterpret_cast<const uint32_t*>(r4 + D / 2 + 4 * dg);
-          const int at = 4 * (2 * ((o >> 2) & 1) + (o & 1)) + (o & 2);
+          const int at = 4 * (2 * (o >> 5) + (o & 1)) + (o & 2);
 #pragma unroll
           for (int d = 0; d < 8; d += 2) {
             const uint32_t v = four_bits((y >> (4 * d) & 15u) | (y >> (4 * d + 4) & 15u) << 16, v_bit(d), v_bit(d + 1));
@@ -415,7 +412,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     }
   } else {
     // -------------------------------------------------------------- softmax
-    const int t = (warp >> 2) + opaque_zero(), np = stream_pages(t);
+    const int t = warp >> 2, np = stream_pages(t);
     const int r0 = 128 * (tile0 + (pair ? t : 0)) + 32 * (warp & 3), r = r0 + lane;
     const int col = 32 * (warp & 3) + lane;
     float* out = p.parts + (static_cast<int64_t>(item) * STREAMS + t) * piece_floats(D, 128);
@@ -468,7 +465,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       const int n_all = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, sees <= 0 ? 0x7FFFFFFFu : static_cast<unsigned>(sees)) / PT);
       float ref = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int k = opaque_zero(); k < np; ++k) {
+      for (int k = 0; k < np; ++k) {
         const int pg = alternate ? 2 * k + t : k, st = pg % NST;
         ok = wait(&sm.s_full[t], k);  // (the page's scales were there before S was begun)
         if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
@@ -527,7 +524,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         const float mr = ref == -INFINITY ? 0.f : ref;
         const float2 kq2 = make_float2(kq, kq), mr2 = make_float2(-mr, -mr);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // the words of P: V's order within 4 tokens is 0, 2, 1, 3
+        // the words of P in V's order: within 4 tokens 0, 2, 1, 3, and 4 tokens of each half in turn
         uint32_t w[PT / 2];
 #pragma unroll
         for (int i = 0; i < PT; i += 4) {
@@ -539,8 +536,10 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
           sum[1] = __fadd2_rn(sum[1], v);
           u = __fmul2_rn(u, make_float2(vs.x, vs.y));
           v = __fmul2_rn(v, make_float2(vs.z, vs.w));
-          w[i / 2] = pack_f16x2(u.x, v.x);
-          w[i / 2 + 1] = pack_f16x2(u.y, v.y);
+          constexpr int kHalf = PT / 2;
+          const int at = 4 * (i % kHalf / 4) + 2 * (i / kHalf);
+          w[at] = pack_f16x2(u.x, v.x);
+          w[at + 1] = pack_f16x2(u.y, v.y);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         tmem_st32(tm + lanes + H::S + t * PT, w);
