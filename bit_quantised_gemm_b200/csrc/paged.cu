@@ -40,8 +40,9 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   const int g = lane % GP, t = lane / GP;
   pdl_wait();
   pdl_trigger();
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp;  // (tile, K or V, head)
-  const int64_t tile = w / (2 * a.H);
+  // (tile, K or V, head); fewer than 2^32 warps but for the very largest calls
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + warp;
+  const int64_t tile = (w >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(w) / static_cast<uint32_t>(2 * a.H)) : w / (2 * a.H);
   const int kvh = static_cast<int>(w - tile * 2 * a.H);
   const bool is_v = kvh >= a.H;
   const int h = is_v ? kvh - static_cast<int>(a.H) : kvh;
@@ -94,7 +95,12 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
     for (int e = 0; e < 4; ++e) {
       uint32_t b[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = __float_as_uint(__fadd_rn(__fmul_rn(value(8 * e + i), inv), 12582916.f));
+      for (int i = 0; i < 8; i += 2) {
+        float lo = value(8 * e + i), hi = value(8 * e + i + 1);
+        mul_then_add_rn(lo, hi, inv, 12582916.f);
+        b[i] = __float_as_uint(lo);
+        b[i + 1] = __float_as_uint(hi);
+      }
       q[e] = pack8(b);
     }
     p[0] = q[0] | q[1] << 24;
