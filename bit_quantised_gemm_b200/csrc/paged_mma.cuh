@@ -156,6 +156,13 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The page's tokens kept at 4 bits among its first `most`, a bit each.
+__device__ __forceinline__ uint64_t tokens4(const float* ksc, int most) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t lo = __ballot_sync(0xFFFFFFFFu, lane < most && signbit(ksc[lane]));
+  const uint32_t hi = __ballot_sync(0xFFFFFFFFu, lane + 32 < most && signbit(ksc[lane + 32]));
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
 // 2^(e - 127) of a biased exponent 1..254
 __device__ __forceinline__ float pow2_biased(int e) { return __int_as_float(e << 23); }
 
@@ -281,10 +288,12 @@ struct F16Page {
         s[u][1][q] = c[2 + q] * ks.y;
       }
     }
-    const bool plain = __all_sync(0xFFFFFFFFu, !(sign >> 31)) && j < n_all;
-    uint32_t four = 0u;  // bit 2 u + r: the lane's token is kept at 4 bits
-    int lim[QC], most = 0;
-    if (!plain) {
+    const bool part = j >= n_all, has4 = __any_sync(0xFFFFFFFFu, sign >> 31);
+    int lim[QC], most = PT;
+#pragma unroll
+    for (int c = 0; c < QC; ++c) lim[c] = PT;
+    if (part) {
+      most = 0;
 #pragma unroll
       for (int c = 0; c < QC; ++c) {
         lim[c] = max(0, min(PT, sees[c] - j * PT));
@@ -297,13 +306,22 @@ struct F16Page {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int o = 16 * u + 2 * g + r;
-          const bool is4 = signbit(ksc[o]);
-          if (is4) four |= 1u << (2 * u + r);
 #pragma unroll
           for (int q = 0; q < QC; ++q)
-            if (is4 || o >= lim[q]) s[u][r][q] = -INFINITY;
-          if (o >= most) { vs[u][r] = 0.f; four &= ~(1u << (2 * u + r)); }  // not a token: whatever is there
+            if (o >= lim[q]) s[u][r][q] = -INFINITY;
+          if (o >= most) vs[u][r] = 0.f;  // not a token: whatever is there
         }
+    }
+    if (has4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 ks = *reinterpret_cast<const float2*>(ksc + 16 * u + 2 * g);
+#pragma unroll
+        for (int q = 0; q < QC; ++q) {
+          if (signbit(ks.x)) s[u][0][q] = -INFINITY;
+          if (signbit(ks.y)) s[u][1][q] = -INFINITY;
+        }
+      }
     }
     // ---- online softmax, in base 2; value scales relative to 2^(ve - 127)
     float m_new[QC];
@@ -398,63 +416,59 @@ struct F16Page {
     }
     // ---- the page's 4-bit tokens, one after the other: lane (g, t4) has dimensions
     // LD g .. LD g + LD - 1 of the rows and its columns' queries
-    if (!plain) {
+    if (has4) {
       const int C4 = a.C4;
-#pragma unroll 1
-      for (int i = 0; i < 8; ++i) {
-        uint32_t set = __ballot_sync(0xFFFFFFFFu, t4 == 0 && ((four >> i) & 1u));
-        for (; set; set &= set - 1u) {
-          const int o = 16 * (i >> 1) + (__ffs(set) - 1) / 2 + (i & 1);
-          const int j4 = blk[o * RB];
-          if (j4 >= C4) {
-            if (lane == 0) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
-            continue;
-          }
-          const uint8_t* r4 = c4_bytes ? blk + block_bytes(D) + j4 * D
-                                       : a.codes4 + ((static_cast<int64_t>(page) * a.H + sg.h) * C4 + j4) * D;
-          uint32_t kc[LD / 8], vc[LD / 8];
+      for (uint64_t set = tokens4(ksc, most); set; set &= set - 1) {
+        const int o = __ffsll(static_cast<long long>(set)) - 1;
+        const int j4 = blk[o * RB];
+        if (j4 >= C4) {
+          if (lane == 0) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
+          continue;
+        }
+        const uint8_t* r4 = c4_bytes ? blk + block_bytes(D) + j4 * D
+                                     : a.codes4 + ((static_cast<int64_t>(page) * a.H + sg.h) * C4 + j4) * D;
+        uint32_t kc[LD / 8], vc[LD / 8];
 #pragma unroll
-          for (int c = 0; c < LD / 8; ++c) {
-            kc[c] = reinterpret_cast<const uint32_t*>(r4 + LD / 2 * g)[c];
-            vc[c] = reinterpret_cast<const uint32_t*>(r4 + D / 2 + LD / 2 * g)[c];
-          }
-          const float k4 = fabsf(ksc[o]) * a.qk_scale * 1.4426950408889634f, v4 = vsc[o];
-          const int vb4 = __float_as_int(v4) >> 23;
-          float fv = 1.f;
-          if (vb4 > ve) {
-            fv = vb4 - ve > 126 ? 0.f : pow2_biased(127 - (vb4 - ve));
-            ve = vb4;
-          }
-          const float v = v4 * pow2_biased(min(268 - ve, 254)) * (1.f / 512.f);
+        for (int c = 0; c < LD / 8; ++c) {
+          kc[c] = reinterpret_cast<const uint32_t*>(r4 + LD / 2 * g)[c];
+          vc[c] = reinterpret_cast<const uint32_t*>(r4 + D / 2 + LD / 2 * g)[c];
+        }
+        const float k4 = fabsf(ksc[o]) * a.qk_scale * 1.4426950408889634f, v4 = vsc[o];
+        const int vb4 = __float_as_int(v4) >> 23;
+        float fv = 1.f;
+        if (vb4 > ve) {
+          fv = vb4 - ve > 126 ? 0.f : pow2_biased(127 - (vb4 - ve));
+          ve = vb4;
+        }
+        const float v = v4 * pow2_biased(min(268 - ve, 254)) * (1.f / 512.f);
 #pragma unroll
-          for (int q = 0; q < QC; ++q) {
-            float dot = 0.f;
-            if (qrow[q] != nullptr) {
+        for (int q = 0; q < QC; ++q) {
+          float dot = 0.f;
+          if (qrow[q] != nullptr) {
 #pragma unroll
-              for (int c = 0; c < LD / 8; ++c) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4*>(qrow[q] + LD * g) + c);
-                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+            for (int c = 0; c < LD / 8; ++c) {
+              const uint4 x = __ldg(reinterpret_cast<const uint4*>(qrow[q] + LD * g) + c);
+              const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int d = 0; d < 8; ++d)
-                  dot = fmaf(__uint_as_float((d & 1) ? (y[d >> 1] & 0xFFFF0000u) : (y[d >> 1] << 16)),
-                             static_cast<float>(static_cast<int>((kc[c] >> (4 * d)) & 15u) - 8), dot);
-              }
+              for (int d = 0; d < 8; ++d)
+                dot = fmaf(__uint_as_float((d & 1) ? (y[d >> 1] & 0xFFFF0000u) : (y[d >> 1] << 16)),
+                           static_cast<float>(static_cast<int>((kc[c] >> (4 * d)) & 15u) - 8), dot);
             }
+          }
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, x);
-            const float sc = o < lim[q] ? dot * k4 : -INFINITY;
-            const float mn = fmaxf(m_run[q], sc);
-            const float f = mn == -INFINITY ? 1.f : ex2(m_run[q] - mn);
-            const float pe = mn == -INFINITY ? 0.f : ex2(sc - mn);
-            m_run[q] = mn;
-            l_run[q] = fmaf(l_run[q], f, g == 0 ? pe : 0.f);
+          for (int x = 4; x < 32; x <<= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, x);
+          const float sc = o < lim[q] ? dot * k4 : -INFINITY;
+          const float mn = fmaxf(m_run[q], sc);
+          const float f = mn == -INFINITY ? 1.f : ex2(m_run[q] - mn);
+          const float pe = mn == -INFINITY ? 0.f : ex2(sc - mn);
+          m_run[q] = mn;
+          l_run[q] = fmaf(l_run[q], f, g == 0 ? pe : 0.f);
 #pragma unroll
-            for (int d = 0; d < LD; ++d) {
-              const float x = static_cast<float>(static_cast<int>((vc[d >> 3] >> (4 * (d & 7))) & 15u) - 8) *
-                              static_cast<float>(1 << v_bit(d & 7));
-              float& y = acc[d >> 1][2 * (d & 1) + q];
-              y = fmaf(pe * v, x, y * (f * fv));
-            }
+          for (int d = 0; d < LD; ++d) {
+            const float x = static_cast<float>(static_cast<int>((vc[d >> 3] >> (4 * (d & 7))) & 15u) - 8) *
+                            static_cast<float>(1 << v_bit(d & 7));
+            float& y = acc[d >> 1][2 * (d & 1) + q];
+            y = fmaf(pe * v, x, y * (f * fv));
           }
         }
       }
@@ -559,6 +573,7 @@ struct I8Page {
   float m_ref, l_run, to_int;  // weights are relative to 2^m_ref, and to_int x as whole numbers
   int acc[NF][4], off[4];
   float o4[FOUR ? LD / 2 : 1];  // 4-bit tokens' part: this lane's half of the dimensions
+  uint32_t q4[2][FOUR ? D / 64 : 1];  // and D / 32 dimensions of both rows' queries for their scores
   int held, w_exp;              // pages in acc; biased exponent behind to_int
   bool any;                     // the piece has been written to
   float* piece;
@@ -622,6 +637,13 @@ struct I8Page {
       const int r = sg.r0 + (t4 >> 1);
       sees = row_sees(a, sg, r);
       qrow = r < sg.rows ? query_row(a, sg, r) : nullptr;
+    }
+    if constexpr (FOUR) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+          q4[r][i] = sg.r0 + r < sg.rows ? __ldg(reinterpret_cast<const uint32_t*>(query_row(a, sg, sg.r0 + r)) + D / 64 * (threadIdx.x & 31) + i) : 0u;
     }
     n_all = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<unsigned>(sees)) / PT);
     m_ref = -INFINITY;
@@ -763,12 +785,11 @@ struct I8Page {
         s[u][r] = f * (r ? ks.y : ks.x);
       }
     }
-    const bool plain = __all_sync(0xFFFFFFFFu, !(sign >> 31)) && j < n_all;
-    uint32_t four = 0u;  // bit 2 u + r: the lane's token is kept at 4 bits
-    int lim = PT;
-    if (!plain) {
+    const bool part = j >= n_all, has4 = __any_sync(0xFFFFFFFFu, sign >> 31);
+    int lim = PT, most = PT;
+    if (part) {
       lim = max(0, min(PT, sees - j * PT));
-      int most = qrow != nullptr ? lim : 0;
+      most = qrow != nullptr ? lim : 0;
       most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
       lim = min(lim, most);
 #pragma unroll
@@ -776,11 +797,17 @@ struct I8Page {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int o = 16 * u + 2 * g + r;
-          const bool is4 = signbit(ksc[o]);
-          if (is4 && o < most) four |= 1u << (2 * u + r);
-          if (is4 || o >= lim) s[u][r] = -INFINITY;
+          if (o >= lim) s[u][r] = -INFINITY;
           if (o >= most) vs[u][r] = 0.f;  // not a token: whatever is there
         }
+    }
+    if (has4) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float2 ks = *reinterpret_cast<const float2*>(ksc + 16 * u + 2 * g);
+        if (signbit(ks.x)) s[u][0] = -INFINITY;
+        if (signbit(ks.y)) s[u][1] = -INFINITY;
+      }
     }
     // ---- weights p x (V scale) as whole numbers; base 2
     float top = s[0][0];
@@ -870,61 +897,55 @@ struct I8Page {
       mma_u8u8(off, 0x04040404u, 0x04040404u, 0x04040404u, 0x04040404u, b[2 * t], b[2 * t + 1]);
     }
     ++held;
-    if (!plain && __any_sync(0xFFFFFFFFu, four != 0u)) four_bit(a, sg, blk, page, four, lim, c4_bytes);
+    if (has4) four_bit(a, sg, blk, page, tokens4(ksc, most), lim, c4_bytes);
   }
 
-  // The page's 4-bit tokens, one after the other: lane (g, t4) has dimensions
-  // LD g .. LD g + LD - 1 of the K row, and half of them of the V row.
-  __device__ __forceinline__ void four_bit(const AttnArgs& a, const Segment& sg, const uint8_t* blk, int page, uint32_t four,
+  // The page's 4-bit tokens, one after the other: a lane has D / 32 dimensions of
+  // the K row for both rows, and half of LD dimensions of the V row for its own.
+  __device__ __forceinline__ void four_bit(const AttnArgs& a, const Segment& sg, const uint8_t* blk, int page, uint64_t set,
                                            int lim, int c4_bytes) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-      uint32_t set = __ballot_sync(0xFFFFFFFFu, t4 == 0 && ((four >> i) & 1u));
-      for (; set; set &= set - 1u) {
-        const int o = 16 * (i >> 1) + (__ffs(set) - 1) / 2 + (i & 1);
-        const int j4 = blk[o * RB];
-        if (!FOUR || j4 >= a.C4) {
-          if (lane == 0) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
-          continue;
+    for (; set; set &= set - 1) {
+      const int o = __ffsll(static_cast<long long>(set)) - 1;
+      const int j4 = blk[o * RB];
+      if (!FOUR || j4 >= a.C4) {
+        if (lane == 0) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
+        continue;
+      }
+      if constexpr (FOUR) {
+        const uint8_t* r4 = c4_bytes ? blk + block_bytes(D) + j4 * D
+                                     : a.codes4 + ((static_cast<int64_t>(page) * a.H + sg.h) * a.C4 + j4) * D;
+        const uint32_t kc = D == 64 ? r4[lane] : D == 128 ? reinterpret_cast<const uint16_t*>(r4)[lane] : reinterpret_cast<const uint32_t*>(r4)[lane];
+        float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) {
+          const float c = static_cast<float>(static_cast<int>((kc >> (4 * d)) & 15u) - 8);
+          d0 = fmaf(__uint_as_float((d & 1) ? (q4[0][d >> 1] & 0xFFFF0000u) : (q4[0][d >> 1] << 16)), c, d0);
+          d1 = fmaf(__uint_as_float((d & 1) ? (q4[1][d >> 1] & 0xFFFF0000u) : (q4[1][d >> 1] << 16)), c, d1);
         }
-        if constexpr (FOUR) {
-          const uint8_t* r4 = c4_bytes ? blk + block_bytes(D) + j4 * D
-                                       : a.codes4 + ((static_cast<int64_t>(page) * a.H + sg.h) * a.C4 + j4) * D;
-          uint32_t kc[LD / 8];
+        // even lanes sum the first row's, odd lanes the second's; then each takes its row's
+        float dot = (lane & 1) ? d1 : d0;
+        dot += __shfl_xor_sync(0xFFFFFFFFu, (lane & 1) ? d0 : d1, 1);
 #pragma unroll
-          for (int c = 0; c < LD / 8; ++c) kc[c] = reinterpret_cast<const uint32_t*>(r4 + LD / 2 * g)[c];
-          float dot = 0.f;
-          if (qrow != nullptr) {
+        for (int x = 2; x < 32; x <<= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, x);
+        dot = __shfl_sync(0xFFFFFFFFu, dot, t4 >> 1);
+        const float k4 = fabsf(reinterpret_cast<const float*>(blk + off_ks(D))[o]) * a.qk_scale * 1.4426950408889634f;
+        const float v4 = reinterpret_cast<const float*>(blk + off_vs(D))[o];
+        const float sc = o < lim ? dot * k4 : -INFINITY;
+        if (__any_sync(0xFFFFFFFFu, sc > m_ref + 20.f)) {
+          flush(fmaxf(m_ref, sc));
+          to_int = INFINITY;  // found anew on the next page
+        }
+        const float e = sc == -INFINITY ? 0.f : ex2(sc - m_ref);
+        if (g == 0) l_run += e;
+        const float ev = e * v4;
+        const uint8_t* vr = r4 + D / 2 + LD / 2 * g + (t4 & 1) * (LD / 4);
 #pragma unroll
-            for (int c = 0; c < LD / 8; ++c) {
-              const uint4 x = __ldg(reinterpret_cast<const uint4*>(qrow + LD * g) + c);
-              const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int d = 0; d < 8; ++d)
-                dot = fmaf(__uint_as_float((d & 1) ? (y[d >> 1] & 0xFFFF0000u) : (y[d >> 1] << 16)),
-                           static_cast<float>(static_cast<int>((kc[c] >> (4 * d)) & 15u) - 8), dot);
-            }
-          }
-#pragma unroll
-          for (int x = 4; x < 32; x <<= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, x);
-          const float k4 = fabsf(reinterpret_cast<const float*>(blk + off_ks(D))[o]) * a.qk_scale * 1.4426950408889634f;
-          const float v4 = reinterpret_cast<const float*>(blk + off_vs(D))[o];
-          const float sc = o < lim ? dot * k4 : -INFINITY;
-          if (__any_sync(0xFFFFFFFFu, sc > m_ref + 20.f)) {
-            flush(fmaxf(m_ref, sc));
-            to_int = INFINITY;  // found anew on the next page
-          }
-          const float e = sc == -INFINITY ? 0.f : ex2(sc - m_ref);
-          if (g == 0) l_run += e;
-          const float ev = e * v4;
-          const uint8_t* vr = r4 + D / 2 + LD / 2 * g + (t4 & 1) * (LD / 4);
-#pragma unroll
-          for (int d = 0; d < LD / 2; d += 2) {
-            const uint32_t c = vr[d / 2];
-            o4[d] = fmaf(ev, static_cast<float>(static_cast<int>(c & 15u) - 8), o4[d]);
-            o4[d + 1] = fmaf(ev, static_cast<float>(static_cast<int>(c >> 4) - 8), o4[d + 1]);
-          }
+        for (int d = 0; d < LD / 2; d += 2) {
+          const uint32_t c = vr[d / 2];
+          o4[d] = fmaf(ev, static_cast<float>(static_cast<int>(c & 15u) - 8), o4[d]);
+          o4[d + 1] = fmaf(ev, static_cast<float>(static_cast<int>(c >> 4) - 8), o4[d + 1]);
         }
       }
     }
