@@ -28,7 +28,7 @@
 // the exponentials need 1024 each: a stream's chain of products, barriers,
 // tensor-memory load, maximum and weights is 3500 long, and tensor memory holds
 // no third stream and no second S. P through shared memory (the next S is then
-// there when a softmax ends) was slower, 105 us against 101 at 96 x 32 heads
+// there when a softmax ends) was slower, 105 us against 101 (98 now) at 96 x 32 heads
 // behind 32768 tokens: the products' operands, the unpackers and the scales
 // already take more than half of what shared memory can move.
 #include "launch.h"
@@ -470,6 +470,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         ok = wait(&sm.s_full[t], k);  // (the page's scales were there before S was begun)
         if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
         tc_fence_after();
+        const uint64_t dead = sm.dead[st];
+        const float v_top = static_cast<float>(sm.v_exp[st] - 133);
         float2 s[PT / 2];
         {
           uint32_t x[PT];
@@ -482,7 +484,6 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
             s[i / 2 + 1] = __fmul2_rn(make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])), make_float2(ks.z, ks.w));
           }
         }
-        const uint64_t dead = sm.dead[st];
         if (pg >= n_all || dead != 0) {
           const int lim = sees - pg * PT;
           const uint64_t on = ~dead & (lim >= PT ? ~0ull : lim <= 0 ? 0ull : (1ull << lim) - 1ull);
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         for (int i = 0; i < PT / 2; ++i) mx[i & 3] = max3(mx[i & 3], s[i].x, s[i].y);
         mx[0] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
         // weights stay below 2^15: p <= 2^8, V scales x 2^(133 - v_exp) below 2^7
-        const float want = mx[0] * kq + static_cast<float>(sm.v_exp[st] - 133);
+        const float want = mx[0] * kq + v_top;
         const bool grow = want > ref + 8.f || (ref == -INFINITY && want > -INFINITY);
         if (__any_sync(0xFFFFFFFFu, grow)) {
           const float now = grow ? want : ref;
