@@ -70,7 +70,7 @@ __device__ __forceinline__ int row_sees(const AttnArgs& a, const Segment& s, int
 // MMA, for a mask, an fma and a share of a shift. The 2^j go into the queries
 // (a power of two: exact) for K, and leave at the end for V.
 // Without the fma (the subnormals as operands, the offset of 4 taken off the
-// sums) it would be 256 of 900 instructions a page less, but the MMA lines its
+// sums) it would be 256 of 1000 instructions a page less, but the MMA lines its
 // products up by the operands' exponents, where all subnormals have 2^-14:
 // with small j, 8 bits of its sums were lost.
 
