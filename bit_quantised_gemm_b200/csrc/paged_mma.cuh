@@ -151,6 +151,8 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
 }
+// a number's upper 11 bits, which are an fp16 number where it is no smaller than 2^-14
+__device__ __forceinline__ float f16_top(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -171,8 +173,12 @@ __device__ __forceinline__ float pow2_biased(int e) { return __int_as_float(e <<
 // contracted index of the values' (V codes^T x weights); query rows are the 8
 // columns of both. QC: columns of a lane that are queries: 1: 4 rows a group
 // (columns 2 q and 2 q + 1 are both row q, of which one is kept: half the
-// softmax), 2: 8. The weights are rounded to fp16 for the value product: 2^-11
-// of a weight, a quarter of what the output's own rounding may take.
+// softmax), 2: 8. A weight goes into the value product as two fp16 numbers, its
+// upper 11 bits and what is left of it, so that 2^-22 of it is lost. (With one number,
+// 2^-11, the outputs of 8 sequences behind 4096 tokens were 8e-4 from those of 32-bit
+// weights, now 5e-5; 8 rows of 64 sequences of up to 4096 tokens 135 us -> 151.)
+// The second part of 4 rows lies in the columns that would be empty, that of 8
+// takes products of its own.
 template <int D, int QC>
 struct F16Page {
   static constexpr int COLS = 4 * QC;
@@ -350,10 +356,10 @@ struct F16Page {
         m_run[q] = m_new[q];
         l_run[q] *= f;
 #pragma unroll
-        for (int m = 0; m < NM; ++m) {
-          acc[m][q] *= f * fv;
-          acc[m][2 + q] *= f * fv;
-        }
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (QC == 1 || (i & 1) == q) acc[m][i] *= f * fv;
       }
     }
     const float vf = pow2_biased(min(268 - ve, 254));  // value scales below 2^15
@@ -364,20 +370,22 @@ struct F16Page {
     // of the 16, of rows 8..15 token 4 t4 + 1 (+ 2): the lane's words of 4 tokens
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      uint32_t b[2];
+      uint32_t b[QC][2];  // 8 rows: the weights' upper parts, then the lower ones
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float v = vs[u][r] * vf;
         const float p0 = ex2(fmaf(s[u][r][0], kq[0], -mr[0]));
         l_run[0] += p0;
+        const float w0 = p0 * v, h0 = f16_top(w0);
         if constexpr (QC == 1) {
-          b[r] = pack_f16x2(p0 * v, 0.f);
+          b[0][r] = transpose8x8(pack_f16x2(h0, w0 - h0));
         } else {
           const float p1 = ex2(fmaf(s[u][r][QC - 1], kq[QC - 1], -mr[QC - 1]));
           l_run[QC - 1] += p1;
-          b[r] = pack_f16x2(p0 * v, p1 * v);
+          const float w1 = p1 * v, h1 = f16_top(w1);
+          b[0][r] = transpose8x8(pack_f16x2(h0, h1));
+          b[QC - 1][r] = transpose8x8(pack_f16x2(w0 - h0, w1 - h1));
         }
-        b[r] = transpose8x8(b[r]);
       }
       const uint8_t* vw = blk + off_v(D) + (4 * u + t4) * 4 * RB + 4 * (3 * LD / 8) * g;
       uint32_t w[LD / 8][3];
@@ -405,7 +413,8 @@ struct F16Page {
         uint32_t x0, x1, y0, y1;                                               \
         v_operand<E_>(w[i], x, x0, x1);                                        \
         v_operand<E_ + 1>(w[i], x, y0, y1);                                    \
-        mma_f16(acc[4 * i + E_ / 2], x0, y0, x1, y1, b[0], b[1]);              \
+        mma_f16(acc[4 * i + E_ / 2], x0, y0, x1, y1, b[0][0], b[0][1]);        \
+        if constexpr (QC == 2) mma_f16(acc[4 * i + E_ / 2], x0, y0, x1, y1, b[QC - 1][0], b[QC - 1][1]); \
       }
 #pragma unroll
       for (int i = 0; i < LD / 8; ++i) {
@@ -469,6 +478,7 @@ struct F16Page {
                             static_cast<float>(1 << v_bit(d & 7));
             float& y = acc[d >> 1][2 * (d & 1) + q];
             y = fmaf(pe * v, x, y * (f * fv));
+            if constexpr (QC == 1) acc[d >> 1][2 * (d & 1) + 1] *= f * fv;
           }
         }
       }
@@ -492,8 +502,9 @@ struct F16Page {
         float x[4];
 #pragma unroll
         for (int d = 0; d < 4; ++d) {
-          const int dl = 4 * c + d;
-          x[d] = acc[dl >> 1][2 * (dl & 1) + q] * (1.f / static_cast<float>(32 << v_bit(dl & 7))) *
+          const int dl = 4 * c + d, at = 2 * (dl & 1);
+          x[d] = (QC == 1 ? acc[dl >> 1][at] + acc[dl >> 1][at + 1] : acc[dl >> 1][at + q]) *
+                 (1.f / static_cast<float>(32 << v_bit(dl & 7))) *
                  pow2_biased(ve) * inv;  // 2^(9 - 14 + ve - 127 - v_bit)
         }
         if (whole) reinterpret_cast<uint2*>(row)[c] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
