@@ -13,13 +13,16 @@
 //               128-byte swizzled; a token kept at 4 bits is one of these rows
 //   scaler      one warp, the scales beside them, and which tokens take part
 //   issuers     a warp a stream, of which one thread issues: S = Q K^T (Q in
-//               tensor memory), O += P V (P in tensor memory, where S was).
+//               tensor memory), O += P V (P's two parts in tensor memory, where S was).
 //               One warp for both streams had each wait for the other's softmax,
 //               and its products queue up, which slows the softmax warps that
 //               share its scheduler
 //   softmax     4 warps a stream, a row a thread: s = S x (K scale),
-//               p = 2^(s - r), weights p x (V scale) rounded to fp16 (2^-11 of a
-//               weight, a quarter of what the output's rounding may take). r is
+//               p = 2^(s - r), weights p x (V scale) as two fp16 numbers each, the
+//               upper 11 bits and what is left (2^-22 of a weight is lost; with
+//               one alone, 2^-11, outputs were 9e-4 from those of 32-bit weights,
+//               now 1e-4). The products of a page's first half run while the
+//               second half's weights are made (134 us if not). r is
 //               the largest s so far plus the largest V scale's exponent; it
 //               moves, and O is multiplied, only when it grows by 8
 // While one stream is in the softmax, the other's products run.
@@ -62,7 +65,7 @@ struct Shared {
   int v_exp[H::NST];      // biased exponent of the largest V scale
   int page[H::NRAW];
   uint64_t raw_full[H::NRAW], raw_empty[H::NRAW], k_full[H::NST], v_full[H::NST], v_empty[H::NST];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], drain[2];
+  uint64_t q_full[2], s_full[2], p_full[2][2], pv_done[2], drain[2];
   uint32_t tmem;
   int abort;
 };
@@ -161,7 +164,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       const int live = (stream_rows(t) + 31) / 32;  // warps with rows
       mbar_init(&sm.q_full[t], live);
       mbar_init(&sm.s_full[t], 1);
-      mbar_init(&sm.p_full[t], live);
+      for (int i = 0; i < 2; ++i) mbar_init(&sm.p_full[t][i], live);
       mbar_init(&sm.pv_done[t], 1);
       mbar_init(&sm.drain[t], 1);
     }
@@ -219,12 +222,22 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
     for (int k = 0; k <= np && ok; ++k) {
       if (k > 0) {  // values of the page before
         const int pg = alternate ? 2 * (k - 1) + t : k - 1, st = pg % NST;
-        if (!(ok = wait_all(&sm.v_full[st], pg / NST) && wait_all(&sm.p_full[t], k - 1))) break;
-        tc_fence_after();
-        if (lead) {
-          const uint32_t vt = v_lo + st * (H::TILE >> 4);
+        const uint32_t vt = v_lo + st * (H::TILE >> 4);
+        ok = wait_all(&sm.v_full[st], pg / NST);
 #pragma unroll
-          for (int i = 0; i < PT / 16; ++i) mma_f16_ts(tm + H::O + t * D, tm + H::S + t * PT + 8 * i, desc_at(vt, 2 * i), idO, k > 1 || i > 0);
+        for (int half = 0; half < 2; ++half) {  // the products of P's first tokens run while the others are made
+          if (!(ok = ok && wait_all(&sm.p_full[t][half], k - 1))) break;
+          tc_fence_after();
+          if (lead) {
+#pragma unroll
+            for (int i = 0; i < PT / 16; ++i) {  // the weights' upper parts, then the lower ones
+              const int at = PT / 32 * half + i % (PT / 32);
+              mma_f16_ts(tm + H::O + t * D, tm + H::S + t * PT + 8 * at + i / (PT / 32) * (PT / 2), desc_at(vt, 2 * at), idO, k > 1 || half > 0 || i > 0);
+            }
+          }
+        }
+        if (!ok) break;
+        if (lead) {
           tc_commit(&sm.pv_done[t]);
           tc_commit(&sm.v_empty[st]);
         }
@@ -525,29 +538,37 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         const float mr = ref == -INFINITY ? 0.f : ref;
         const float2 kq2 = make_float2(kq, kq), mr2 = make_float2(-mr, -mr);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // the words of P in V's order: within 4 tokens 0, 2, 1, 3, and 4 tokens of each half in turn
-        uint32_t w[PT / 2];
+        // the words of P in V's order: within 4 tokens 0, 2, 1, 3, and 4 tokens of each half of the page in turn
 #pragma unroll
-        for (int i = 0; i < PT; i += 4) {
-          const float4 vs = *reinterpret_cast<const float4*>(&sm.vs[st][i]);
-          float2 u = __ffma2_rn(s[i / 2], kq2, mr2), v = __ffma2_rn(s[i / 2 + 1], kq2, mr2);
-          u = make_float2(ex2(u.x), ex2(u.y));
-          v = make_float2(ex2(v.x), ex2(v.y));
-          sum[0] = __fadd2_rn(sum[0], u);
-          sum[1] = __fadd2_rn(sum[1], v);
-          u = __fmul2_rn(u, make_float2(vs.x, vs.y));
-          v = __fmul2_rn(v, make_float2(vs.z, vs.w));
-          constexpr int kHalf = PT / 2;
-          const int at = 4 * (i % kHalf / 4) + 2 * (i / kHalf);
-          w[at] = pack_f16x2(u.x, v.x);
-          w[at + 1] = pack_f16x2(u.y, v.y);
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[PT / 4], lo[PT / 4];
+#pragma unroll
+          for (int at = 0; at < PT / 4; at += 2) {
+            const int i = PT / 4 * half + at / 4 * 4 + PT / 2 * (at / 2 % 2);
+            const float4 vs = *reinterpret_cast<const float4*>(&sm.vs[st][i]);
+            float2 u = __ffma2_rn(s[i / 2], kq2, mr2), v = __ffma2_rn(s[i / 2 + 1], kq2, mr2);
+            u = make_float2(ex2(u.x), ex2(u.y));
+            v = make_float2(ex2(v.x), ex2(v.y));
+            sum[0] = __fadd2_rn(sum[0], u);
+            sum[1] = __fadd2_rn(sum[1], v);
+            u = __fmul2_rn(u, make_float2(vs.x, vs.y));
+            v = __fmul2_rn(v, make_float2(vs.z, vs.w));
+            const float2 ut = make_float2(f16_top(u.x), f16_top(u.y)), vt = make_float2(f16_top(v.x), f16_top(v.y));
+            w[at] = pack_f16x2(ut.x, vt.x);
+            w[at + 1] = pack_f16x2(ut.y, vt.y);
+            u = __fadd2_rn(u, make_float2(-ut.x, -ut.y));
+            v = __fadd2_rn(v, make_float2(-vt.x, -vt.y));
+            lo[at] = pack_f16x2(u.x, v.x);
+            lo[at + 1] = pack_f16x2(u.y, v.y);
+          }
+          tmem_st16(tm + lanes + H::S + t * PT + PT / 4 * half, w);
+          tmem_st16(tm + lanes + H::S + t * PT + PT / 2 + PT / 4 * half, lo);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm.p_full[t][half]);
         }
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_st32(tm + lanes + H::S + t * PT, w);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.p_full[t]);
       }
       // ---- the piece
       if (ok && np > 0) {

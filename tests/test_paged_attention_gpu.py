@@ -70,3 +70,9 @@ def few_tokens(D, form):
 @pytest.mark.parametrize("form", OWN + FEW)
 def test_weights_to_half_a_step(D, form):
     few_tokens(D, form)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("form", TILES)
+def test_tile_weights_to_half_a_step(D, form):
+    few_tokens(D, form)
