@@ -158,6 +158,14 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// What weights p = 2^(score - reference) are taken relative to, for a largest score: not below it (p <= 1), and 8 above
+// it, so that scores a little larger do not move it. Far out, where 8 would be lost, the score itself.
+__device__ __forceinline__ float reference(float score) { return fabsf(score) < 1048576.f ? ceilf(score) + 8.f : score; }
+// The exponent e for a largest weight w = p x (V scale): w 2^-e lies in [2^7, 2^8). It grows with w, to kMostWeight;
+// weights that are next to nothing beside p (2^-100) need none of their own.
+constexpr float kLeastExp = -100.f, kMostWeight = 32768.f;
+__device__ __forceinline__ float weight_exp(float w) { return fmaxf(static_cast<float>((__float_as_int(w) >> 23) - 134), kLeastExp); }
+
 // The page's tokens kept at 4 bits among its first `most`, a bit each.
 __device__ __forceinline__ uint64_t tokens4(const float* ksc, int most) {
   const int lane = threadIdx.x & 31;
@@ -179,6 +187,12 @@ __device__ __forceinline__ float pow2_biased(int e) { return __int_as_float(e <<
 // weights, now 5e-5; 8 rows of 64 sequences of up to 4096 tokens 135 us -> 151.)
 // The second part of 4 rows lies in the columns that would be empty, that of 8
 // takes products of its own.
+// Two references a row: weights of the sum are relative to 2^m_run, a bound of
+// the scores so far; those of the values, p x (V scale), are besides relative to
+// 2^w_exp, which follows the largest of THEM: the largest V scale may be that of a
+// token without weight. The largest is 2^7 to 2^15, so what is lost of the others
+// for want of exponents (2^-24) is 2^-31 of it or less. References move when a
+// score or a weight outgrows them, for which no lane needs the others' on most pages.
 template <int D, int QC>
 struct F16Page {
   static constexpr int COLS = 4 * QC;
@@ -188,11 +202,12 @@ struct F16Page {
   static constexpr int KW = D == 64 ? 2 : 3;                // stream words of a lane's chunk
 
   uint32_t qb[2 * NB];   // query operands: pair i of this lane's chunk of column g
-  float kq[QC];          // what makes of (sum) x (K scale) a score in base 2
+  float kq[QC];          // what makes of (sum) x (K scale) x c0 a score in base 2: a power of two, so that the
+                         // largest score is exactly what its weight's exponent has taken off
+  float c0;
   int sees[QC], n_all;   // tokens that the lane's columns see; pages before n_all are seen whole by all columns
   const uint16_t* qrow[QC];
-  float m_run[QC], l_run[QC], acc[NM][4];
-  int ve;                // biased exponent that value scales are taken relative to (at least that of 2^-113)
+  float m_run[QC], l_run[QC], w_exp[QC], acc[NM][4];  // acc: value sums / 2^(m_run + w_exp)
 
   __device__ __forceinline__ void begin(const AttnArgs& a, const Segment& sg, float*) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
@@ -225,7 +240,8 @@ struct F16Page {
         const int jl = 3 * pr.lo - pr.n, jh = 3 * pr.hi - pr.n - 16;
         qb[i] = pack_f16x2(qf(d0 + pr.lo) * (1.f / (1 << jl)), qf(d0 + pr.hi) * (1.f / (1 << jh)));
       }
-      const float kr = a.qk_scale * 1.4426950408889634f * pow2_biased(263 - fb);  // 2^(9 + 127 - fb)
+      c0 = a.qk_scale * 1.4426950408889634f;
+      const float kr = pow2_biased(263 - fb);  // 2^(9 + 127 - fb)
 #pragma unroll
       for (int c = 0; c < QC; ++c) {
         const int src = QC == 1 ? 8 * t4 : 4 * (2 * t4 + c);  // a lane of the column's row
@@ -236,15 +252,42 @@ struct F16Page {
       }
     }
 #pragma unroll
-    for (int c = 0; c < QC; ++c) { m_run[c] = -INFINITY; l_run[c] = 0.f; }
+    for (int c = 0; c < QC; ++c) { m_run[c] = -INFINITY; l_run[c] = 0.f; w_exp[c] = kLeastExp; }
 #pragma unroll
     for (int m = 0; m < NM; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][i] = 0.f;
-    ve = 14;
     n_all = sees[0];
     if constexpr (QC == 2) n_all = min(n_all, sees[QC - 1]);
     n_all = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, static_cast<unsigned>(n_all)) / PT);
+  }
+
+  // A score in base 2 above m_run: takes the sum along; returns the factor of the value sums.
+  __device__ __forceinline__ float more_score(int q, float score) {
+    if (!(score > m_run[q])) return 1.f;
+    const float m = reference(score), d = m_run[q] - m;
+    l_run[q] *= ex2(d);
+    m_run[q] = m;
+    w_exp[q] += d;  // the value sums stay as they are
+    if (w_exp[q] >= kLeastExp) return 1.f;
+    const float f = ex2(w_exp[q] - kLeastExp);
+    w_exp[q] = kLeastExp;
+    return f;
+  }
+  // The same for a weight p x (V scale) that 2^w_exp does not hold.
+  __device__ __forceinline__ float more_weight(int q, float w) {
+    const float e = weight_exp(w);
+    if (!(e > w_exp[q])) return 1.f;
+    const float f = ex2(w_exp[q] - e);
+    w_exp[q] = e;
+    return f;
+  }
+  __device__ __forceinline__ void scale_values(int q, float f) {
+#pragma unroll
+    for (int m = 0; m < NM; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (QC == 1 || (i & 1) == q) acc[m][i] *= f;
   }
 
   // page number j of the segment; c4_bytes: of the page's 4-bit rows behind the block (0: none, or in global memory)
@@ -290,8 +333,8 @@ struct F16Page {
       sign |= __float_as_uint(ks.x) | __float_as_uint(ks.y);
 #pragma unroll
       for (int q = 0; q < QC; ++q) {
-        s[u][0][q] = c[q] * ks.x;
-        s[u][1][q] = c[2 + q] * ks.y;
+        s[u][0][q] = c[q] * (ks.x * c0);
+        s[u][1][q] = c[2 + q] * (ks.y * c0);
       }
     }
     const bool part = j >= n_all, has4 = __any_sync(0xFFFFFFFFu, sign >> 31);
@@ -329,43 +372,41 @@ struct F16Page {
         }
       }
     }
-    // ---- online softmax, in base 2; value scales relative to 2^(ve - 127)
-    float m_new[QC];
-    bool grew = false;
-#pragma unroll
-    for (int q = 0; q < QC; ++q) {
-      float mt = s[0][0][q];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) mt = fmaxf(mt, s[i >> 1][i & 1][q]);
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xFFFFFFFFu, mt, o));
-      m_new[q] = fmaxf(m_run[q], mt * kq[q]);
-      grew = grew || m_new[q] > m_run[q];
-    }
+    // ---- references, in base 2
     float vm = vs[0][0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) vm = fmaxf(vm, vs[i >> 1][i & 1]);
-    const int vb = __reduce_max_sync(0xFFFFFFFFu, __float_as_int(vm)) >> 23;
-    if (__any_sync(0xFFFFFFFFu, grew || vb > ve)) {
-      const int vn = max(ve, vb);
-      const float fv = vn - ve > 126 ? 0.f : pow2_biased(127 - (vn - ve));
-      ve = vn;
+    float mt[QC];
+    bool more = false;
+#pragma unroll
+    for (int q = 0; q < QC; ++q) {
+      mt[q] = s[0][0][q];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) mt[q] = fmaxf(mt[q], s[i >> 1][i & 1][q]);
+      mt[q] *= kq[q];  // (exact)
+      more = more || mt[q] > m_run[q] || (mt[q] > -INFINITY && !(ex2(mt[q] - m_run[q]) * vm * ex2(-w_exp[q]) < kMostWeight));
+    }
+    if (__any_sync(0xFFFFFFFFu, more)) {
 #pragma unroll
       for (int q = 0; q < QC; ++q) {
-        const float f = m_new[q] == -INFINITY ? 1.f : ex2(m_run[q] - m_new[q]);
-        m_run[q] = m_new[q];
-        l_run[q] *= f;
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+        for (int o = 4; o < 32; o <<= 1) mt[q] = fmaxf(mt[q], __shfl_xor_sync(0xFFFFFFFFu, mt[q], o));
+        float f = more_score(q, mt[q]), top = 0.f;
+        const float mr = m_run[q] == -INFINITY ? 0.f : m_run[q];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (QC == 1 || (i & 1) == q) acc[m][i] *= f * fv;
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, ex2(fmaf(s[i >> 1][i & 1][q], kq[q], -mr)) * vs[i >> 1][i & 1]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+        f *= more_weight(q, top);
+        scale_values(q, f);
       }
     }
-    const float vf = pow2_biased(min(268 - ve, 254));  // value scales below 2^15
-    float mr[QC];
+    float mr[QC], wf[QC];
 #pragma unroll
-    for (int q = 0; q < QC; ++q) mr[q] = m_run[q] == -INFINITY ? 0.f : m_run[q];
+    for (int q = 0; q < QC; ++q) {
+      mr[q] = m_run[q] == -INFINITY ? 0.f : m_run[q];
+      wf[q] = ex2(-w_exp[q]);
+    }
     // ---- weights and values; B's token 2 t4 (+ 1) of rows 0..7 is token 4 t4 (+ 2)
     // of the 16, of rows 8..15 token 4 t4 + 1 (+ 2): the lane's words of 4 tokens
 #pragma unroll
@@ -373,31 +414,30 @@ struct F16Page {
       uint32_t b[QC][2];  // 8 rows: the weights' upper parts, then the lower ones
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float v = vs[u][r] * vf;
         const float p0 = ex2(fmaf(s[u][r][0], kq[0], -mr[0]));
         l_run[0] += p0;
-        const float w0 = p0 * v, h0 = f16_top(w0);
+        const float w0 = p0 * vs[u][r] * wf[0], h0 = f16_top(w0);
         if constexpr (QC == 1) {
           b[0][r] = transpose8x8(pack_f16x2(h0, w0 - h0));
         } else {
           const float p1 = ex2(fmaf(s[u][r][QC - 1], kq[QC - 1], -mr[QC - 1]));
           l_run[QC - 1] += p1;
-          const float w1 = p1 * v, h1 = f16_top(w1);
+          const float w1 = p1 * vs[u][r] * wf[QC - 1], h1 = f16_top(w1);
           b[0][r] = transpose8x8(pack_f16x2(h0, h1));
           b[QC - 1][r] = transpose8x8(pack_f16x2(w0 - h0, w1 - h1));
         }
       }
       const uint8_t* vw = blk + off_v(D) + (4 * u + t4) * 4 * RB + 4 * (3 * LD / 8) * g;
-      uint32_t w[LD / 8][3];
+      uint32_t vc[LD / 8][3];
       if constexpr (D == 64) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) w[0][i] = reinterpret_cast<const uint32_t*>(vw)[i];
+        for (int i = 0; i < 3; ++i) vc[0][i] = reinterpret_cast<const uint32_t*>(vw)[i];
       } else if constexpr (D == 128) {
 #pragma unroll
         for (int i = 0; i < 3; ++i) {
           const uint2 x = reinterpret_cast<const uint2*>(vw)[i];
-          w[(2 * i) / 3][(2 * i) % 3] = x.x;
-          w[(2 * i + 1) / 3][(2 * i + 1) % 3] = x.y;
+          vc[(2 * i) / 3][(2 * i) % 3] = x.x;
+          vc[(2 * i + 1) / 3][(2 * i + 1) % 3] = x.y;
         }
       } else {
 #pragma unroll
@@ -405,20 +445,20 @@ struct F16Page {
           const uint4 x = reinterpret_cast<const uint4*>(vw)[i];
           const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-          for (int c = 0; c < 4; ++c) w[(4 * i + c) / 3][(4 * i + c) % 3] = y[c];
+          for (int c = 0; c < 4; ++c) vc[(4 * i + c) / 3][(4 * i + c) % 3] = y[c];
         }
       }
 #define BLT_V(E_)                                                                    \
       {                                                                        \
         uint32_t x0, x1, y0, y1;                                               \
-        v_operand<E_>(w[i], x, x0, x1);                                        \
-        v_operand<E_ + 1>(w[i], x, y0, y1);                                    \
+        v_operand<E_>(vc[i], x, x0, x1);                                       \
+        v_operand<E_ + 1>(vc[i], x, y0, y1);                                   \
         mma_f16(acc[4 * i + E_ / 2], x0, y0, x1, y1, b[0][0], b[0][1]);        \
         if constexpr (QC == 2) mma_f16(acc[4 * i + E_ / 2], x0, y0, x1, y1, b[QC - 1][0], b[QC - 1][1]); \
       }
 #pragma unroll
       for (int i = 0; i < LD / 8; ++i) {
-        const uint32_t x[3] = {w[i][0] >> 8, w[i][1] >> 8, w[i][2] >> 8};
+        const uint32_t x[3] = {vc[i][0] >> 8, vc[i][1] >> 8, vc[i][2] >> 8};
         BLT_V(0) BLT_V(2) BLT_V(4) BLT_V(6)
       }
 #undef BLT_V
@@ -442,14 +482,9 @@ struct F16Page {
           kc[c] = reinterpret_cast<const uint32_t*>(r4 + LD / 2 * g)[c];
           vc[c] = reinterpret_cast<const uint32_t*>(r4 + D / 2 + LD / 2 * g)[c];
         }
-        const float k4 = fabsf(ksc[o]) * a.qk_scale * 1.4426950408889634f, v4 = vsc[o];
-        const int vb4 = __float_as_int(v4) >> 23;
-        float fv = 1.f;
-        if (vb4 > ve) {
-          fv = vb4 - ve > 126 ? 0.f : pow2_biased(127 - (vb4 - ve));
-          ve = vb4;
-        }
-        const float v = v4 * pow2_biased(min(268 - ve, 254)) * (1.f / 512.f);
+        const float k4 = fabsf(ksc[o]) * c0, v4 = vsc[o];
+        float sc[QC];
+        bool more = false;
 #pragma unroll
         for (int q = 0; q < QC; ++q) {
           float dot = 0.f;
@@ -466,19 +501,27 @@ struct F16Page {
           }
 #pragma unroll
           for (int x = 4; x < 32; x <<= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, x);
-          const float sc = o < lim[q] ? dot * k4 : -INFINITY;
-          const float mn = fmaxf(m_run[q], sc);
-          const float f = mn == -INFINITY ? 1.f : ex2(m_run[q] - mn);
-          const float pe = mn == -INFINITY ? 0.f : ex2(sc - mn);
-          m_run[q] = mn;
-          l_run[q] = fmaf(l_run[q], f, g == 0 ? pe : 0.f);
+          sc[q] = o < lim[q] ? dot * k4 : -INFINITY;
+          more = more || sc[q] > m_run[q] || !(v4 * ex2(-w_exp[q]) < 0x1p60f);  // (its weight is not rounded to fewer bits)
+        }
+        if (__any_sync(0xFFFFFFFFu, more)) {
+#pragma unroll
+          for (int q = 0; q < QC; ++q) {
+            const float f = more_score(q, sc[q]);
+            scale_values(q, f * more_weight(q, sc[q] == -INFINITY ? 0.f : ex2(sc[q] - m_run[q]) * v4));
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < QC; ++q) {
+          const float pe = sc[q] == -INFINITY ? 0.f : ex2(sc[q] - m_run[q]);
+          if (g == 0) l_run[q] += pe;
+          const float v = pe * v4 * ex2(-w_exp[q]) * (1.f / 512.f);
 #pragma unroll
           for (int d = 0; d < LD; ++d) {
             const float x = static_cast<float>(static_cast<int>((vc[d >> 3] >> (4 * (d & 7))) & 15u) - 8) *
                             static_cast<float>(1 << v_bit(d & 7));
             float& y = acc[d >> 1][2 * (d & 1) + q];
-            y = fmaf(pe * v, x, y * (f * fv));
-            if constexpr (QC == 1) acc[d >> 1][2 * (d & 1) + 1] *= f * fv;
+            y = fmaf(v, x, y);
           }
         }
       }
@@ -495,7 +538,7 @@ struct F16Page {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
       if (qrow[q] == nullptr) continue;
-      const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : 0.f;
+      const float vf = ex2(w_exp[q]) * (!whole ? 1.f : l > 0.f ? 1.f / l : 0.f);
       uint16_t* row = output_row(a, sg, sg.r0 + col) + LD * g;
 #pragma unroll
       for (int c = 0; c < LD / 4; ++c) {
@@ -504,8 +547,7 @@ struct F16Page {
         for (int d = 0; d < 4; ++d) {
           const int dl = 4 * c + d, at = 2 * (dl & 1);
           x[d] = (QC == 1 ? acc[dl >> 1][at] + acc[dl >> 1][at + 1] : acc[dl >> 1][at + q]) *
-                 (1.f / static_cast<float>(32 << v_bit(dl & 7))) *
-                 pow2_biased(ve) * inv;  // 2^(9 - 14 + ve - 127 - v_bit)
+                 (512.f / static_cast<float>(1 << v_bit(dl & 7))) * vf;
         }
         if (whole) reinterpret_cast<uint2*>(row)[c] = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
         else reinterpret_cast<float4*>(out + col * D + LD * g)[c] = make_float4(x[0], x[1], x[2], x[3]);

@@ -404,8 +404,8 @@ int kv_pages_compact(uint8_t* pages, int64_t page_bytes, uint8_t* codes4, int64_
  *   out[b,i,hq] = bf16_rne(sum_t p_t v_t), zero where no token is seen
  * with k, v dequantised from the pages (code * scale), sums in 32 bits. A
  * token's weight p_t x (V scale) enters the products as a whole number (up to
- * 2 rows of a head: 2^-30 of the largest weight is lost) or as two 16-bit
- * floats (2^-22 of the weight is lost).
+ * 2 rows of a head) or as two 16-bit floats: 2^-22 of it or 2^-30 of the row's
+ * largest weight, whichever is more, may be lost.
  *   q        device bf16 [B x Sq x Hq x D], tokens (b, i) ldq elements apart
  *   pages, codes4   one layer's pool
  *   shared   device int32 [n_shared], nullable iff n_shared == 0

@@ -76,3 +76,91 @@ def test_weights_to_half_a_step(D, form):
 @pytest.mark.parametrize("form", TILES)
 def test_tile_weights_to_half_a_step(D, form):
     few_tokens(D, form)
+
+
+# ------------------------------------------------------ range of the weights
+def lopsided(rng, n_pages, H, D, at, k_at, v_exp):
+    """Pages in which the tokens `at` have a key whose only large value is k_at, and values 2^v_exp in size."""
+    x = C.normal(rng, n_pages, H, D)
+    x[0, :, :, 0] = 0
+    for t in at:
+        x[0, t] = 0
+        x[0, t, :, 0] = k_at
+        x[1, t] *= np.float32(2.0 ** v_exp)
+    return C.write(rng, x[0], x[1], n_pages, 2, plain=[t % 64 for t in at])
+
+
+def lopsided_sets(D, form, at, k_at, v_exp):
+    """Every row's query is 8 in dimension 0, which the other keys leave at zero: the tokens `at` have scores of
+    8 k_at / sqrt(D). 4 pages in order, in front or not."""
+    Bn, G, Sq, front = form
+    rng = np.random.default_rng(D + Bn + G + Sq + abs(v_exp))
+    H = 2
+    pages, codes4 = lopsided(rng, 4, H, D, at, k_at, v_exp)
+    x = rng.standard_normal((Bn, Sq, H * G, D), np.float32)
+    x[..., 0] = 8
+    q = O.f32_to_bf16(x)
+    lens = rng.integers(Sq, 256, Bn)
+    lens[0], lens[1] = 256, 150
+    if front:
+        check(pages, codes4, q, np.zeros((Bn, 0), int), lens, [0, 1, 2, 3])
+        check(pages, codes4, q, np.tile([2, 3], (Bn, 1)), lens, [0, 1])
+    else:
+        check(pages, codes4, q, np.tile([0, 1, 2, 3], (Bn, 1)), lens)
+
+
+RANGES = [([5], -4096.0, 28), ([5], -4096.0, 40), ([70, 140], -4096.0, 60), ([0, 63, 128], -65536.0, 100),
+          ([0], 30.0, -60), ([70], 60.0, -60), ([0, 100], 12.0, 20), ([3, 190], 200.0, -30)]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("form", OWN + FEW)
+@pytest.mark.parametrize("at,k_at,v_exp", RANGES)
+def test_range_of_weights(D, form, at, k_at, v_exp):
+    """Tokens without weight and with large values, or that take nearly all and have values of nearly nothing."""
+    lopsided_sets(D, form, at, k_at, v_exp)
+
+
+def spread_values(D, form):
+    """Values between 2^-13 and 2^13 in size, sharp and flat scores."""
+    Bn, G, Sq, front = form
+    rng = np.random.default_rng(D + Bn + G + Sq)
+    H = 2
+    x = C.normal(rng, 4, H, D)
+    x[1] *= np.exp(3 * rng.standard_normal((256, H, 1), np.float32))
+    pages, codes4 = C.write(rng, x[0], x[1], 4, 1)
+    lens = rng.integers(Sq, 257, Bn)
+    for gain in (0, 1, 8):
+        q = O.f32_to_bf16(gain * rng.standard_normal((Bn, Sq, H * G, D), np.float32))
+        check(pages, codes4, q, np.tile([0, 1, 2, 3][2 * front:], (Bn, 1)), lens, [0, 1][:2 * front])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("form", OWN + FEW)
+def test_spread_values(D, form):
+    spread_values(D, form)
+
+
+def unwritten_pages(D, Bn, n):
+    """Pages of a new pool (scales of zero) counted among the tokens: scores of zero, values of zero."""
+    rng = np.random.default_rng(D + Bn)
+    H = 2
+    pages, codes4 = C.pool(rng, 6, H, D, 1)
+    pages[0], codes4[0] = 0, 0
+    shared = np.zeros(n, int)
+    shared[10::25] = 1 + rng.integers(0, 5, len(shared[10::25]))
+    q = W.normal_bf16(rng, (Bn, 1, H, D))
+    lens = rng.integers(64 * 40, 64 * n, Bn)
+    kv = R.dequant(pages, codes4)
+    o, E = R.attention(q, kv, np.zeros((Bn, 0), int), lens, shared)
+    got = run(pages, codes4, q, np.zeros((Bn, 0), int), lens, shared)
+    # a piece has n / 18 pages at most where there are tiles, n / 100 in a walk
+    err, most = np.abs(got - o), R.bound(o, E, 8 * n // 18 + 160)
+    worst = (int((err > most).sum()), err.size, float((err / most).max()))
+    assert worst[0] == 0, worst
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Bn", [2, 4, 16])
+def test_unwritten_pages(D, Bn):
+    unwritten_pages(D, Bn, 400)
