@@ -18,13 +18,18 @@
 //               and its products queue up, which slows the softmax warps that
 //               share its scheduler
 //   softmax     4 warps a stream, a row a thread: s = S x (K scale),
-//               p = 2^(s - r), weights p x (V scale) as two fp16 numbers each, the
-//               upper 11 bits and what is left (2^-22 of a weight is lost; with
-//               one alone, 2^-11, outputs were 9e-4 from those of 32-bit weights,
-//               now 1e-4). The products of a page's first half run while the
-//               second half's weights are made (134 us if not). r is
-//               the largest s so far plus the largest V scale's exponent; it
-//               moves, and O is multiplied, only when it grows by 8
+//               p = 2^(s - m), weights p x (V scale) / 2^e as two fp16 numbers
+//               each, the upper 11 bits and what is left (2^-22 of a weight is
+//               lost; with one alone, 2^-11, outputs were 9e-4 from those of
+//               32-bit weights, now 1e-4). The products of a page's first half
+//               run while the second half's weights are made (142 us if not).
+//               m bounds the scores so far and moves when one is above it. e
+//               follows the largest weight, so that tokens without weight and
+//               with large values do not press the others out of fp16's range,
+//               and moves, and O is multiplied, when one reaches 2^15. A page's
+//               largest score and V scale say whether one may: only then are
+//               the weights themselves looked at. (Both in one reference, by
+//               the page's largest V scale: 126 us, where this takes 128.)
 // While one stream is in the softmax, the other's products run.
 //
 // A page of two tiles takes 3500 clocks at D = 128, where the tensor pipe and
@@ -62,7 +67,7 @@ struct Shared {
   using H = Shape<D>;
   float ks[H::NST][PT], vs[H::NST][PT];
   uint64_t dead[H::NST];  // tokens that take no part
-  int v_exp[H::NST];      // biased exponent of the largest V scale
+  int v_exp[H::NST];      // the V scales are below 2^v_exp
   int page[H::NRAW];
   uint64_t raw_full[H::NRAW], raw_empty[H::NRAW], k_full[H::NST], v_full[H::NST], v_empty[H::NST];
   uint64_t q_full[2], s_full[2], p_full[2][2], pv_done[2], drain[2];
@@ -279,7 +284,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       const float* scales = reinterpret_cast<const float*>(src + off_ks(D));
       const int live = sm.page[rs] < 0 ? 0 : min(PT, seen - (first + pg) * PT);
       uint32_t dead[2];
-      int top = 14;
+      int top = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int o = lane + 32 * i;
@@ -288,13 +293,13 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         const bool bad4 = use && signbit(ks) && src[o * RB] >= a.C4;
         if (bad4) report_status(a.status, BITLINEAR_STATUS_BAD_INDEX);
         dead[i] = __ballot_sync(0xFFFFFFFFu, !use || bad4);
-        sm.ks[st][o] = use ? fabsf(ks) : 0.f;
+        sm.ks[st][o] = use ? fabsf(ks) * (a.qk_scale * 1.4426950408889634f) : 0.f;
         sm.vs[st][o] = use ? vs : 0.f;
         if (use) top = max(top, __float_as_int(vs) >> 23);
       }
       top = __reduce_max_sync(0xFFFFFFFFu, top);
       if (lane == 0) {
-        sm.v_exp[st] = top;
+        sm.v_exp[st] = top - 126;
         sm.dead[st] = static_cast<uint64_t>(dead[1]) << 32 | dead[0];
       }
       __syncwarp();
@@ -451,7 +456,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         }
         const int fb = min(268 - max(1, static_cast<int>(am >> 7)), 254);
         const float f = pow2_biased(fb);
-        kq = a.qk_scale * 1.4426950408889634f * pow2_biased(263 - fb);
+        kq = pow2_biased(263 - fb);
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {  // 32 dimensions
           uint32_t x[16], y[16];
@@ -476,7 +481,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
       // pages before n_all are seen whole by all rows that see anything (a slot of the batch without a
       // request would send its warp through the masks on every page)
       const int n_all = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, sees <= 0 ? 0x7FFFFFFFu : static_cast<unsigned>(sees)) / PT);
-      float ref = -INFINITY, l = 0.f;
+      float m = -INFINITY, e = kLeastExp, l = 0.f;
       bool ok = true;
       for (int k = 0; k < np; ++k) {
         const int pg = alternate ? 2 * k + t : k, st = pg % NST;
@@ -484,7 +489,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
         tc_fence_after();
         const uint64_t dead = sm.dead[st];
-        const float v_top = static_cast<float>(sm.v_exp[st] - 133);
+        const float v_top = static_cast<float>(sm.v_exp[st]);
         float2 s[PT / 2];
         {
           uint32_t x[PT];
@@ -511,13 +516,33 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
 #pragma unroll
         for (int i = 0; i < PT / 2; ++i) mx[i & 3] = max3(mx[i & 3], s[i].x, s[i].y);
         mx[0] = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-        // weights stay below 2^15: p <= 2^8, V scales x 2^(133 - v_exp) below 2^7
-        const float want = mx[0] * kq + v_top;
-        const bool grow = want > ref + 8.f || (ref == -INFINITY && want > -INFINITY);
-        if (__any_sync(0xFFFFFFFFu, grow)) {
-          const float now = grow ? want : ref;
-          const float f = ref == -INFINITY ? 0.f : ex2(ref - now);
-          if (k > 0) {
+        const float top = mx[0] * kq;  // (exact)
+        if (__any_sync(0xFFFFFFFFu, top > m || top - m + v_top - e > 15.f)) {
+          float f = 1.f;  // of the value sums
+          if (top > m) {
+            const float now = reference(top), d = m - now;
+            l *= ex2(d);
+            m = now;
+            e += d;
+            if (e < kLeastExp) {
+              f = ex2(e - kLeastExp);
+              e = kLeastExp;
+            }
+          }
+          float w = 0.f;
+          const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll
+          for (int i = 0; i < PT; i += 4) {
+            const float4 vs = *reinterpret_cast<const float4*>(&sm.vs[st][i]);
+            w = max3(w, ex2(fmaf(s[i / 2].x, kq, -mr)) * vs.x, ex2(fmaf(s[i / 2].y, kq, -mr)) * vs.y);
+            w = max3(w, ex2(fmaf(s[i / 2 + 1].x, kq, -mr)) * vs.z, ex2(fmaf(s[i / 2 + 1].y, kq, -mr)) * vs.w);
+          }
+          if (!(w * ex2(-e) < kMostWeight)) {
+            const float now = weight_exp(w);
+            f *= ex2(e - now);
+            e = now;
+          }
+          if (k > 0 && __any_sync(0xFFFFFFFFu, f != 1.f)) {
             ok = wait(&sm.pv_done[t], k - 1);
             if (!__all_sync(0xFFFFFFFFu, ok)) { ok = false; break; }
             tc_fence_after();
@@ -532,11 +557,9 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
             }
             tmem_st_wait();
           }
-          l *= f;
-          ref = now;
         }
-        const float mr = ref == -INFINITY ? 0.f : ref;
-        const float2 kq2 = make_float2(kq, kq), mr2 = make_float2(-mr, -mr);
+        const float mr = m == -INFINITY ? 0.f : m, wf = ex2(-e);
+        const float2 kq2 = make_float2(kq, kq), mr2 = make_float2(-mr, -mr), wf2 = make_float2(wf, wf);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         // the words of P in V's order: within 4 tokens 0, 2, 1, 3, and 4 tokens of each half of the page in turn
 #pragma unroll
@@ -551,8 +574,8 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
             v = make_float2(ex2(v.x), ex2(v.y));
             sum[0] = __fadd2_rn(sum[0], u);
             sum[1] = __fadd2_rn(sum[1], v);
-            u = __fmul2_rn(u, make_float2(vs.x, vs.y));
-            v = __fmul2_rn(v, make_float2(vs.z, vs.w));
+            u = __fmul2_rn(__fmul2_rn(u, make_float2(vs.x, vs.y)), wf2);
+            v = __fmul2_rn(__fmul2_rn(v, make_float2(vs.z, vs.w)), wf2);
             const float2 ut = make_float2(f16_top(u.x), f16_top(u.y)), vt = make_float2(f16_top(v.x), f16_top(v.y));
             w[at] = pack_f16x2(ut.x, vt.x);
             w[at + 1] = pack_f16x2(ut.y, vt.y);
@@ -577,6 +600,7 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
         tc_fence_after();
       }
       if (ok) {
+        const float vf = ex2(e);
         if (np > 0)
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -585,13 +609,13 @@ __global__ void __launch_bounds__(Shape<D>::THREADS, 1) front_kernel(const __gri
             tmem_ld_wait();
             if (r < rows) {
               float4* dst = reinterpret_cast<float4*>(out + col * D + 32 * c);
-              auto o = [&](int i) { return __uint_as_float(x[i]) * (512.f / static_cast<float>(1 << v_bit(i & 7))); };
+              auto o = [&](int i) { return __uint_as_float(x[i]) * (512.f / static_cast<float>(1 << v_bit(i & 7))) * vf; };
 #pragma unroll
               for (int i = 0; i < 8; ++i) dst[i] = make_float4(o(4 * i), o(4 * i + 1), o(4 * i + 2), o(4 * i + 3));
             }
           }
         if (r < rows) {
-          out[128 * D + col] = sees > 0 ? ref : -INFINITY;
+          out[128 * D + col] = sees > 0 ? m : -INFINITY;
           out[128 * D + 128 + col] = sees > 0 ? l : 0.f;
         }
       }

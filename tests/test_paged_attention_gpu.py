@@ -121,6 +121,13 @@ def test_range_of_weights(D, form, at, k_at, v_exp):
     lopsided_sets(D, form, at, k_at, v_exp)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("form", TILES)
+@pytest.mark.parametrize("at,k_at,v_exp", RANGES)
+def test_tile_range_of_weights(D, form, at, k_at, v_exp):
+    lopsided_sets(D, form, at, k_at, v_exp)
+
+
 def spread_values(D, form):
     """Values between 2^-13 and 2^13 in size, sharp and flat scores."""
     Bn, G, Sq, front = form
@@ -138,6 +145,12 @@ def spread_values(D, form):
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("form", OWN + FEW)
 def test_spread_values(D, form):
+    spread_values(D, form)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("form", TILES)
+def test_tile_spread_values(D, form):
     spread_values(D, form)
 
 
@@ -164,3 +177,9 @@ def unwritten_pages(D, Bn, n):
 @pytest.mark.parametrize("Bn", [2, 4, 16])
 def test_unwritten_pages(D, Bn):
     unwritten_pages(D, Bn, 400)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Bn", [17, 200])
+def test_tile_unwritten_pages(D, Bn):
+    unwritten_pages(D, Bn, 900)
