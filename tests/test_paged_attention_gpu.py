@@ -43,6 +43,10 @@ def check(pages, codes4, q, tables, lens, shared=(), steps=64):
     assert worst[0] == 0, worst
 
 
+def check_case(c):
+    check(c.pages, c.codes4, c.q, c.tables, c.lens, c.shared, c.steps)
+
+
 # how rows of a head come together: (sequences, query heads a cache head, queries, pages in front)
 OWN = [(24, 1, 1, 0), (24, 2, 1, 0), (24, 3, 1, 0), (24, 4, 1, 0), (24, 5, 1, 0), (24, 8, 1, 0), (8, 4, 3, 0)]
 FEW = [(2, 1, 1, 1), (4, 1, 1, 1), (3, 2, 1, 1), (16, 1, 1, 1)]
@@ -183,3 +187,51 @@ def test_unwritten_pages(D, Bn):
 @pytest.mark.parametrize("Bn", [17, 200])
 def test_tile_unwritten_pages(D, Bn):
     unwritten_pages(D, Bn, 900)
+
+
+# ------------------------------------------------- several pages to a warp
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G,Sq,C4", [(1, 1, 0), (1, 1, 1), (2, 1, 5), (3, 1, 1), (4, 1, 5), (5, 1, 0), (8, 1, 5), (2, 3, 1)])
+def test_many_sequences(D, G, Sq, C4):
+    """Shares of several pages that begin and end inside sequences and hold several of them; 4-bit rows that
+    travel with their pages and rows that do not."""
+    check_case(C.many_sequences(D, G, C4, Sq=Sq))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 8])
+@pytest.mark.parametrize("graded", [False, True])
+def test_long_sequences(D, G, graded):
+    """24 x 8 heads of 40 to 60 pages: about 4 pages a warp (8 with D = 256), all of one segment; largest score
+    and largest weight moving with every page."""
+    check_case(C.long_sequences(D, G, graded=graded))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [2, 4, 7, 16])
+@pytest.mark.parametrize("graded", [False, True])
+def test_long_prefix_walks(D, rows, graded):
+    """A prefix of 500 pages x 8 heads for few rows: 3 to 7 pages a warp."""
+    check_case(C.long_prefix(D, rows, n=500, H=8, graded=graded))
+    check_case(C.long_prefix(D, rows, n=300, H=16, own=3, graded=graded, C4=5))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [17, 128, 200, 300])
+@pytest.mark.parametrize("graded", [False, True])
+def test_long_prefix_tiles(D, rows, graded):
+    """Tiles over 3 to 8 pages each, a single tile, a pair, and a pair with a single one; with D = 256 one by one."""
+    check_case(C.long_prefix(D, rows, n=300, graded=graded))
+    check_case(C.long_prefix(D, rows, n=301, own=2, graded=graded, C4=0 if graded else 5))
+
+
+@pytest.mark.parametrize("G", [4, 8])
+@pytest.mark.parametrize("D,shared", [(64, 0), (128, 0), (256, 0), (128, 2)])
+def test_many_rows_of_4_bits_in_small_groups(D, G, shared):
+    """Five tokens of a page at 4 bits, more than travel with it, for 4 and 8 rows a head."""
+    rng = np.random.default_rng(D + G + shared)
+    H, Bn = 2, 2 if shared else 6
+    pages, codes4 = C.pool(rng, 8, H, D, 5)
+    lens = 64 * shared + rng.integers(1, 180, Bn)
+    q = W.normal_bf16(rng, (Bn, 1, H * G, D))
+    check(pages, codes4, q, rng.integers(0, 8, (Bn, 3)), lens, rng.permutation(8)[:shared])

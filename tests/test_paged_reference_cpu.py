@@ -1,5 +1,5 @@
 """The 64-bit attention that the paged kernels are held against, on the CPU: against
-the oracle's token by token."""
+the oracle's token by token, and that its bound sees a page that is left out."""
 import numpy as np
 import pytest
 
@@ -25,3 +25,24 @@ def test_against_the_oracle(D, C4):
         want, want_A = P.attention(q, pages, codes4, tables, lens, shared)
         assert np.allclose(o, want, rtol=1e-12, atol=1e-13) and np.allclose(A, want_A, rtol=1e-12, atol=1e-13)
         assert (A.max(-1) <= L[..., 0] * (8 if C4 else 4)).all()
+
+
+def moved(case, skip):
+    """Rows of a case that a page left out at place `skip` moves beyond twice the bound."""
+    kv = R.dequant(case.pages, case.codes4)
+    args = (case.q, kv, case.tables, case.lens, case.shared)
+    o, E = R.attention(*args)
+    lost = R.attention(*args, skip=skip)[0]
+    return (np.abs(lost - o) > 2 * R.bound(o, E, case.steps)).any(-1)
+
+
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 4), (256, 2)])
+def test_the_bound_sees_a_page(D, G):
+    case = C.many_sequences(D, G, 0, B=30, H=2)
+    full = case.lens >= 64 * 4
+    assert full.any() and moved(case, 2)[full].mean() > 0.95
+    case = C.long_sequences(D, G, B=3, H=2)
+    assert moved(case, 21).mean() > 0.6
+    case = C.long_prefix(D, 40)
+    sees = case.lens >= 64 * 31
+    assert moved(case, 30)[sees].mean() > 0.5
