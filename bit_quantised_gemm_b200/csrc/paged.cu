@@ -488,6 +488,7 @@ static cudaError_t pages_copy(const paged::CopyArgs& a, cudaStream_t s, bool beh
   const int64_t pieces = (a.page_bytes + paged::kCopyPiece - 1) / paged::kCopyPiece +
                          (a.page_bytes4 + paged::kCopyPiece - 1) / paged::kCopyPiece;
   const int64_t want = a.n * a.L * pieces, cap = 8LL * num_sms();
+  if (want == 0) return cudaSuccess;  // no layer, or no page to move: a kernel behind waits for the one before
   const dim3 grid(static_cast<unsigned>(want < cap ? want : cap));
   return behind ? launch_behind(paged::copy_kernel, grid, dim3(256), 0, s, a)
                 : launch_kernel(paged::copy_kernel, grid, dim3(256), 0, s, 0u, a);
