@@ -488,7 +488,7 @@ def _paged():
         try:
             from . import _bind as m
         except ImportError as e:
-            raise RuntimeError(f"{_HERE}/_bind.so cannot be loaded ({e}): build it with "
+            raise RuntimeError(f"the module _bind in {_HERE} cannot be loaded ({e}): build it with "
                                "`python -m bit_quantised_gemm_b200.build`") from e
         names = [n for n in _SIGS if n.startswith("kv_")]
         m.setup(_check, status_buffer, {n: _c.cast(getattr(lib(), n), _P).value for n in names})

@@ -1,5 +1,6 @@
 """Build the CUDA library (libbitlinear.so) in-tree with nvcc for sm_100a, and the
-paged-cache calls' binding (_bind.so) with the host compiler.
+paged-cache calls' binding (_bind.<Python's ABI>.so) with the host compiler, where torch
+and Python's headers are there: the library does without them.
 
     python -m bit_quantised_gemm_b200.build [--verbose]
 
@@ -9,16 +10,19 @@ division and multiplication and on round-to-nearest-even conversions.
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libbitlinear.so")
-BIND = os.path.join(PKG, "_bind.so")
+BIND = os.path.join(PKG, "_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
+BIND_RECORD = os.path.join(PKG, "_build", "bind.txt")  # what BIND has been built with
 SOURCES = ["api.cu", "quant.cu", "gemm.cu", "gemv.cu", "gemv_mma.cu", "gemv_dp4a.cu", "attn.cu", "paged.cu", "paged_attn.cu",
            "paged_front.cu", "peak.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -36,6 +40,37 @@ def _stale(out: str, deps: list[str]) -> bool:
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def build_binding(verbose: bool = False, force: bool = False) -> bool:
+    """Build _bind where its source, torch or Python have changed; False if torch or a header is missing."""
+    include = sysconfig.get_paths()["include"]
+    torch = importlib.util.find_spec("torch")  # located, not imported
+    missing = ([] if torch else ["torch"]) + ([] if os.path.exists(os.path.join(include, "Python.h")) else ["Python's headers"])
+    if missing:
+        print(f"the binding of the paged-cache calls is not built: no {' and no '.join(missing)}", file=sys.stderr)
+        return False
+    t = os.path.dirname(torch.origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc_path()))
+    src = os.path.join(CSRC, "bind.cpp")
+    # the system's g++, whose C++ runtime is torch's: a statically linked one breaks exceptions
+    cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           "-I", os.path.join(t, "include"), "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", include, src, "-o", BIND,
+           "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    record = " ".join(cmd) + "\n" + open(os.path.join(t, "version.py")).read()
+    known = open(BIND_RECORD).read() if os.path.exists(BIND_RECORD) else ""
+    if not force and record == known and not _stale(BIND, [src, os.path.join(ROOT, "include", "bitlinear.h")]):
+        return True
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    with open(BIND_RECORD, "w") as f:
+        f.write(record)
+    untagged = os.path.join(PKG, "_bind.so")  # of a build before the ABI was in the name
+    if os.path.exists(untagged):
+        os.remove(untagged)
+    return True
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -62,21 +97,7 @@ def build(verbose: bool = False, force: bool = False) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
-    src = os.path.join(CSRC, "bind.cpp")
-    if force or _stale(BIND, [src, os.path.join(ROOT, "include", "bitlinear.h")]):
-        import sysconfig
-
-        import torch
-        t = os.path.dirname(torch.__file__)
-        cuda = os.path.dirname(os.path.dirname(nvcc))
-        # the system's g++, whose C++ runtime is torch's: a statically linked one breaks exceptions
-        cmd = [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-               "-I", os.path.join(t, "include"), "-I", os.path.join(t, "include", "torch", "csrc", "api", "include"),
-               "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"], src, "-o", BIND,
-               "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        subprocess.run(cmd, check=True)
+    build_binding(verbose, force)
     return LIB
 
 
