@@ -104,9 +104,10 @@ Tables need_tables(const Tensor& tables, const Tensor& lens) {
 class Call {
  public:
   Call(const Tensor& lead, PyObject* status, PyObject* stream, std::initializer_list<std::pair<const char*, const Tensor*>> others) {
+    const Tensor& st = maybe(status, "status");
+    TORCH_CHECK_VALUE(!st.defined() || (st.scalar_type() == at::kInt && st.numel() > 0), "status: must be an int32 tensor of one value");
     TORCH_CHECK_VALUE(lead.is_cuda(), "expected a CUDA tensor");
     const at::Device dev = lead.device();
-    const Tensor& st = maybe(status, "status");
     for (const auto& [name, t] : others) on(dev, name, *t);
     on(dev, "status", st);
     if (st.defined()) {
