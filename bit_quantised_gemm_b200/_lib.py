@@ -551,7 +551,8 @@ def kv_pages_free(tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor, 
 def kv_pages_compact(pages: torch.Tensor, tables: torch.Tensor, lens: torch.Tensor, refs: torch.Tensor,
                      codes4: torch.Tensor | None = None, status=None, stream=None) -> torch.Tensor:
     """Move the pages in use to the front of the pool, in every layer and table;
-    returns their number (int32 [1] on the device)."""
+    returns their number (int32 [1] on the device). A list of shared pages taken
+    before names other pages after: take it again from a row that holds them."""
     return _paged().compact(pages, tables, lens, refs, codes4, status, stream)
 
 

@@ -385,6 +385,9 @@ int kv_pages_free(int32_t* tables, int64_t R, int64_t W, int64_t ldt, int32_t* l
  * Move the n_live pages in use to the front of the pool: the k-th free page
  * below n_live takes the k-th page in use at or above it (in all L layers),
  * and the tables of all R rows follow.
+ * Page ids that are kept elsewhere do not: after the call, take the list of a
+ * shared prefix (kv_attention_3bit_paged's `shared`) again from the table of a
+ * row that holds it. The old list names other pages, and no call can tell.
  *   n_live   device int32 [1], written: the pages from n_live on are free
  *   work     device int32 [2 n_pages + 3], written
  */

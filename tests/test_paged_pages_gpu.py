@@ -1,7 +1,13 @@
-"""The page calls of the paged 3-bit cache on the GPU: pools without layers or pages."""
-from test_paged_gpu import Both
-
+"""The page calls of the paged 3-bit cache on the GPU: pools without layers or pages, and a
+prefix whose pages compaction moves."""
+import numpy as np
 import pytest
+import torch
+
+import bit_quantised_gemm_b200 as B
+from oracle import paged_oracle as P
+from test_paged_gpu import DEV, Both
+import workloads as W
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +33,29 @@ def test_a_pool_without_pages(L, C4):
     b.grow([3], [0])
     b.free([0])
     b.compact()
+
+
+@pytest.mark.parametrize("kids,D", [(3, 128), (18, 64)])
+def test_a_prefix_after_compaction(kids, D):
+    """The prefix's pages move; its list, taken again from a row that holds it, names them: the same answer."""
+    b = Both(kids + 7, 6, 80, L=1, H=2, D=D, C4=0)
+    rng = np.random.default_rng(D)
+    k, v = (W.normal_bf16(rng, (80 * 64, 2, D)) for _ in range(2))
+    P.append(b.o.pages[0], None, k, v, np.arange(80 * 64))
+    b.pages.copy_(torch.from_numpy(b.o.pages))
+    others, first = list(range(kids + 1, kids + 7)), list(range(kids + 1))
+    b.grow(others + [0], [330] * 6 + [260])  # 36 pages, then the prefix's
+    b.fork([0] * kids, first[1:])
+    b.grow(first, [1 + i % 50 for i in first])
+    q = W.bf16_bits_to_torch(W.normal_bf16(rng, (kids + 1, 1, 4, D))).to(DEV)
+
+    def attention(shared):
+        return B.kv_attention_3bit_paged(q, b.pages[0], b.tables[:kids + 1, 4:], b.lens[:kids + 1].contiguous(), shared=shared, status=b.st)
+
+    before = b.tables[0, :4].clone()
+    want = attention(before)
+    b.free(others)
+    b.compact()
+    after = b.tables[0, :4].clone()
+    assert not torch.equal(before, after)
+    assert torch.equal(attention(after), want) and b.st.item() == 0
