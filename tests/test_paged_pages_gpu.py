@@ -1,12 +1,13 @@
-"""The page calls of the paged 3-bit cache on the GPU: pools without layers or pages, and a
-prefix whose pages compaction moves."""
+"""The page calls of the paged 3-bit cache on the GPU: pools without layers or pages, a
+prefix whose pages compaction moves, bad entries alone."""
 import numpy as np
 import pytest
 import torch
 
 import bit_quantised_gemm_b200 as B
+from bit_quantised_gemm_b200 import _lib
 from oracle import paged_oracle as P
-from test_paged_gpu import DEV, Both
+from test_paged_gpu import DEV, Both, ints
 import workloads as W
 
 pytestmark = pytest.mark.gpu
@@ -59,3 +60,31 @@ def test_a_prefix_after_compaction(kids, D):
     after = b.tables[0, :4].clone()
     assert not torch.equal(before, after)
     assert torch.equal(attention(after), want) and b.st.item() == 0
+
+
+def test_bad_entries_change_nothing():
+    """Calls of bad entries alone: every table, length, count and page stays, what unused entries hold too."""
+    b = Both(6, 2, 12)
+    b.grow([0, 1], [100, 64])
+    b.fork([1], [4])
+    kept = [t.clone() for t in (b.wide, b.lens, b.refs, b.pages, b.codes4)]
+
+    def same():
+        assert b.st.item() == _lib.STATUS_BAD_INDEX
+        b.st.zero_()
+        assert all(torch.equal(x, y) for x, y in zip(kept, (b.wide, b.lens, b.refs, b.pages, b.codes4)))
+
+    tables = (b.tables, b.lens, b.refs)
+    for row, n in ((6, 1), (-1, 1), (0, 29), (3, 30), (2, -1)):  # no row, too many for a row, for the call, none
+        got = B.kv_pages_grow(b.pages, *tables, ints([row]), ints([n]), 29, codes4=b.codes4, status=b.st)
+        assert (got == -1).all()
+        same()
+    for parent, child in ((0, 1), (0, 6), (9, 5), (-1, 5), (5, 5)):  # a child with tokens, no row, its own parent
+        B.kv_pages_fork(*tables, ints([parent]), ints([child]), status=b.st)
+        same()
+    for row, keep in ((7, 0), (-3, 0), (0, -1)):
+        B.kv_pages_free(*tables, ints([row]), keep=ints([keep]), status=b.st)
+        same()
+    for src, dst in ((0, 12), (12, 1), (-1, 3), (3, -1)):
+        B.kv_pages_copy(b.pages, ints([src]), ints([dst]), codes4=b.codes4, status=b.st)
+        same()
