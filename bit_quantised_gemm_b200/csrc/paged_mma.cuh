@@ -681,12 +681,13 @@ struct I8Page {
           }
           if (b % 3 == 1) qb[c * NK + 3 * KW] |= digit(d0 + 5, k_field(1, 3)) << (8 * (b & 3));
         }
-      const float kr = a.qk_scale * 1.4426950408889634f * pow2_biased(254 - fb);
+      // (2^27 of the sums' size is taken off them and put here: they lie below 2^11, and a K scale of up to 2^117 fits)
+      const float kr = a.qk_scale * 1.4426950408889634f * pow2_biased(281 - fb);
       const int src = 16 * (t4 >> 1);  // a lane of the row's columns
       kq = __shfl_sync(0xFFFFFFFFu, kr, src);
       sum = __shfl_sync(0xFFFFFFFFu, sum, src);
-      f_mul = (t4 & 1) ? 65536.f : 1.f;
-      f_add = (t4 & 1) ? 0.f : -4.f * sum;
+      f_mul = (t4 & 1) ? 0x1p-11f : 0x1p-27f;
+      f_add = (t4 & 1) ? 0.f : -0x1p-25f * sum;
       const int r = sg.r0 + (t4 >> 1);
       sees = row_sees(a, sg, r);
       qrow = r < sg.rows ? query_row(a, sg, r) : nullptr;

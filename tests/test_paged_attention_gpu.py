@@ -189,6 +189,21 @@ def test_tile_unwritten_pages(D, Bn):
     unwritten_pages(D, Bn, 900)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("form", OWN + FEW + TILES)
+@pytest.mark.parametrize("e", [96, -12])
+def test_keys_and_queries_of_far_sizes(D, form, e):
+    """Keys of 2^e and queries of 2^-e: scores of ordinary size."""
+    Bn, G, Sq, front = form
+    rng = np.random.default_rng(D + Bn + G + Sq)
+    H = 2
+    x = C.normal(rng, 4, H, D)
+    pages, codes4 = C.write(rng, x[0] * np.float32(2.0 ** e), x[1], 4, 1)
+    q = O.f32_to_bf16(np.float32(2.0 ** -e) * rng.standard_normal((Bn, Sq, H * G, D), np.float32))
+    lens = rng.integers(Sq, 257, Bn)
+    check(pages, codes4, q, np.tile([0, 1, 2, 3][2 * front:], (Bn, 1)), lens, [0, 1][:2 * front])
+
+
 # ------------------------------------------------- several pages to a warp
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("G,Sq,C4", [(1, 1, 0), (1, 1, 1), (2, 1, 5), (3, 1, 1), (4, 1, 5), (5, 1, 0), (8, 1, 5), (2, 3, 1)])
