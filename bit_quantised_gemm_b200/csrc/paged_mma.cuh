@@ -620,7 +620,8 @@ struct I8Page {
   static constexpr int kFlushPages = 512;                // 64 tokens x 255 x 224 a page: below 2^31
 
   uint32_t qb[NC * NK];
-  float kq, f_mul, f_add;  // row t4 / 2: sums -> score / K scale: digits 0, 1 (t4 even) and 2, 3 meet, less 4 sum q
+  float kq, f_mul, f_add;  // row t4 / 2: sums -> score / K scale / kq: digits 0, 1 (t4 even) and 2, 3 meet, less 4 sum q;
+                           // kq is a power of two, so that a largest score is exactly what its weight's exponent has taken off
   int sees, n_all;
   const uint16_t* qrow;
   float m_ref, l_run, to_int;  // weights are relative to 2^m_ref, and to_int x as whole numbers
@@ -682,12 +683,13 @@ struct I8Page {
           if (b % 3 == 1) qb[c * NK + 3 * KW] |= digit(d0 + 5, k_field(1, 3)) << (8 * (b & 3));
         }
       // (2^27 of the sums' size is taken off them and put here: they lie below 2^11, and a K scale of up to 2^117 fits)
-      const float kr = a.qk_scale * 1.4426950408889634f * pow2_biased(281 - fb);
+      const float kr = pow2_biased(281 - fb);
       const int src = 16 * (t4 >> 1);  // a lane of the row's columns
       kq = __shfl_sync(0xFFFFFFFFu, kr, src);
       sum = __shfl_sync(0xFFFFFFFFu, sum, src);
-      f_mul = (t4 & 1) ? 0x1p-11f : 0x1p-27f;
-      f_add = (t4 & 1) ? 0.f : -0x1p-25f * sum;
+      const float c0 = a.qk_scale * 1.4426950408889634f;
+      f_mul = (t4 & 1) ? 0x1p-11f * c0 : 0x1p-27f * c0;
+      f_add = (t4 & 1) ? 0.f : -0x1p-25f * c0 * sum;
       const int r = sg.r0 + (t4 >> 1);
       sees = row_sees(a, sg, r);
       qrow = r < sg.rows ? query_row(a, sg, r) : nullptr;

@@ -204,6 +204,33 @@ def test_keys_and_queries_of_far_sizes(D, form, e):
     check(pages, codes4, q, np.tile([0, 1, 2, 3][2 * front:], (Bn, 1)), lens, [0, 1][:2 * front])
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("form", OWN + FEW + TILES)
+@pytest.mark.parametrize("e", [4, 16, 28, 40])
+def test_scores_far_out(D, form, e):
+    """Scores up to 2^(e + 17): the token of the largest one, twice the next, takes all, and the row is its value to
+    half a step and 2^-16, with nothing lost of the score's own weight."""
+    Bn, G, Sq, front = form
+    rng = np.random.default_rng(D + Bn + G + Sq + e)
+    H = 2
+    x = C.normal(rng, 4, H, D)
+    x[0] = 0
+    x[0, :, :, 0] = 2.0 ** 13 * rng.uniform(1, 2, (256, H))
+    x[0, 100, :, 0] = 2.0 ** 15
+    pages, codes4 = C.write(rng, x[0], x[1], 4)
+    q = np.zeros((Bn, Sq, H * G, D), np.float32)
+    q[..., 0] = 2.0 ** e
+    lens = rng.integers(120, 257, Bn)
+    want = R.dequant(pages)[1][1, :, 36].repeat(G, 0)  # [Hq, D]
+    most = np.abs(want) * 2.0 ** -16 + 2.0 ** (np.frexp(np.abs(want) + 2.0 ** -60)[1] - 9.0)
+    sets = [(np.tile([0, 1, 2, 3], (Bn, 1)), [])]
+    if front:
+        sets = [(np.zeros((Bn, 0), int), [0, 1, 2, 3]), (np.tile([2, 3], (Bn, 1)), [0, 1]), (np.tile([1, 2, 3], (Bn, 1)), [0])]
+    for tables, shared in sets:
+        got = run(pages, codes4, O.f32_to_bf16(q), tables, lens, shared)
+        assert (np.abs(got - want) <= most).all()
+
+
 # ------------------------------------------------- several pages to a warp
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("G,Sq,C4", [(1, 1, 0), (1, 1, 1), (2, 1, 5), (3, 1, 1), (4, 1, 5), (5, 1, 0), (8, 1, 5), (2, 3, 1)])
