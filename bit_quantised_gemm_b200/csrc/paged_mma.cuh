@@ -573,7 +573,9 @@ struct F16Page {
 // dimension) or are taken out of the whole numbers at the end (V: the rows of
 // the product are the fields). The other operands are 32-bit fixed-point
 // numbers in 4 digits of 8 bits, a column each: 8 columns are 2 rows.
-//   * queries: 2^-23 of the row's largest value or less is lost;
+//   * queries: a field at bit b takes q 2^-b as a whole number, with the row's largest q
+//     in [2^27, 2^28): 2^(b - 1) is lost, 2^-25 of the largest or less at bits 0 to 3,
+//     2^-21 at bit 7 (the lowest bit of code 5);
 //   * weights p x (V scale): whole numbers below 2^32, 2^32 being 4 to 8 times
 //     the largest so far: sums of codes x weights are exact, zeros add zero.
 // When a weight outgrows that, or the score by 2^20 the one that weights are
