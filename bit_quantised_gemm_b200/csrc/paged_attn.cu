@@ -9,8 +9,8 @@
 //   * the sequences' own pages: the Sq Hq / H rows of a sequence that read
 //     one cache head are the columns of its pages' products;
 //   * the shared pages: the rows of ALL sequences are their columns, so a
-//     shared page is read once for the batch (once for every 8 rows; from 17
-//     rows on paged_front.cu has them, 128 a tile);
+//     shared page is read once for the batch (once for every 8 rows; from
+//     tile_rows() on paged_front.cu has them, 128 a tile);
 //   * a walk leaves, for each stretch of pages that a warp took of one (head,
 //     group of columns), the running maximum, sum and value sums ("a piece");
 //     the join adds a row's pieces of both walks.
@@ -422,14 +422,17 @@ static FrontPlan plan_tiles(int64_t D, int64_t rows, int64_t H, int64_t n) {
   return p;
 }
 
-// Rows from which the tensor-core kernel takes the shared pages. Walk / tiles, whole call in us, D = 128:
-// 64 pages x 32 heads 8 rows 36 / 38, 16 rows 37 / 39, 32 rows 46 / 40; 256 pages x 8 heads 43 / 36, 42 / 36, 48 / 40.
-constexpr int64_t kTileRows = 17;
+// Rows from which the tensor-core kernel takes the shared pages. Walk / tiles, whole call in us:
+//   D = 128, 64 pages x 32 heads   24 rows 39 / 45, 32 rows 42 / 46, 40 rows 47 / 46, 56 rows 58 / 48
+//   D = 128, 256 pages x 8 heads   24 rows 37 / 42, 32 rows 39 / 42, 40 rows 44 / 44, 56 rows 55 / 45
+//   D = 64, 64 pages x 32 heads    24 rows 29 / 37, 32 rows 31 / 37, 40 rows 33 / 38, 56 rows 42 / 39
+//   D = 256, 64 pages x 32 heads   17 rows 59 / 61, 32 rows 72 / 63; with a 4-bit token a page 85 / 66, 106 / 68
+constexpr int64_t tile_rows(int64_t D) { return D == 256 ? 17 : 33; }
 
 static Plan make_plan(int64_t B, int64_t Sq, int64_t Hq, int64_t H, int64_t D, int64_t n_shared, int64_t W) {
   Plan p{};
   const int64_t rows = Sq * (Hq / H);
-  const bool tiled = n_shared > 0 && B * rows >= kTileRows;
+  const bool tiled = n_shared > 0 && B * rows >= tile_rows(D);
   const int per_sm = W > 0 && n_shared > 0 && !tiled ? 1 : 2;
   p.own = plan_walk(D, rows, B * H, B * W * H, W > 0, per_sm);
   if (tiled) p.tiles = plan_tiles(D, B * rows, H, n_shared);

@@ -49,8 +49,8 @@ def check_case(c):
 
 # how rows of a head come together: (sequences, query heads a cache head, queries, pages in front)
 OWN = [(24, 1, 1, 0), (24, 2, 1, 0), (24, 3, 1, 0), (24, 4, 1, 0), (24, 5, 1, 0), (24, 8, 1, 0), (8, 4, 3, 0)]
-FEW = [(2, 1, 1, 1), (4, 1, 1, 1), (3, 2, 1, 1), (16, 1, 1, 1)]
-TILES = [(17, 1, 1, 1), (40, 4, 1, 1), (20, 4, 4, 1)]
+FEW = [(2, 1, 1, 1), (4, 1, 1, 1), (3, 2, 1, 1), (16, 1, 1, 1), (32, 1, 1, 1)]
+TILES = [(17, 1, 1, 1), (33, 1, 1, 1), (40, 4, 1, 1), (20, 4, 4, 1)]
 
 
 # ------------------------------------------------------- bits of the weights
@@ -184,7 +184,7 @@ def test_unwritten_pages(D, Bn):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("Bn", [17, 200])
+@pytest.mark.parametrize("Bn", [17, 40, 200])
 def test_tile_unwritten_pages(D, Bn):
     unwritten_pages(D, Bn, 900)
 
@@ -250,7 +250,7 @@ def test_long_sequences(D, G, graded):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("rows", [2, 4, 7, 16])
+@pytest.mark.parametrize("rows", [2, 4, 7, 16, 32])
 @pytest.mark.parametrize("graded", [False, True])
 def test_long_prefix_walks(D, rows, graded):
     """A prefix of 500 pages x 8 heads for few rows: 3 to 7 pages a warp."""
@@ -259,7 +259,7 @@ def test_long_prefix_walks(D, rows, graded):
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
-@pytest.mark.parametrize("rows", [17, 128, 200, 300])
+@pytest.mark.parametrize("rows", [17, 40, 128, 200, 300])
 @pytest.mark.parametrize("graded", [False, True])
 def test_long_prefix_tiles(D, rows, graded):
     """Tiles over 3 to 8 pages each, a single tile, a pair, and a pair with a single one; with D = 256 one by one."""
