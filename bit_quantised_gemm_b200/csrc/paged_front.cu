@@ -32,13 +32,15 @@
 //               the page's largest V scale: 126 us, where this takes 128.)
 // While one stream is in the softmax, the other's products run.
 //
-// A page of two tiles takes 3500 clocks at D = 128, where the tensor pipe and
-// the exponentials need 1024 each: a stream's chain of products, barriers,
-// tensor-memory load, maximum and weights is 3500 long, and tensor memory holds
-// no third stream and no second S. P through shared memory (the next S is then
-// there when a softmax ends) was slower, 105 us against 101 (98 now) at 96 x 32 heads
-// behind 32768 tokens: the products' operands, the unpackers and the scales
-// already take more than half of what shared memory can move.
+// A page of two tiles takes about 4000 clocks at D = 128 (96 sequences x 32 query
+// heads on 8 cache heads behind 32768 tokens: 43 pages in 188000 clocks of a CTA,
+// beginning and end included), where the tensor pipe needs 1536 and the
+// exponentials 1024: a stream's chain of products, barriers, tensor-memory load,
+// maximum and weights is that long, and tensor memory holds no third stream and no
+// second S. While a weight was one number and a page 3500 clocks, P through shared
+// memory (the next S is then there when a softmax ends) was slower, 105 us against
+// 101: the products' operands, the unpackers and the scales already take more than
+// half of what shared memory can move.
 #include "launch.h"
 #include "paged.cuh"
 #include "paged_mma.cuh"
